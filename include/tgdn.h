@@ -76,14 +76,23 @@ typedef enum {
   TGDN_SEQ_TOO_DEEP = 5,    /* some depth > depth_max */
   TGDN_SEQ_TIMEOUT = 6,     /* a bounded device wait expired; outputs of the
                                sequence are unspecified */
-  TGDN_SEQ_BAD_RANGE = 7    /* cu_nodes[b] < 0, cu_nodes[b+1] < cu_nodes[b] or
+  TGDN_SEQ_BAD_RANGE = 7,   /* cu_nodes[b] < 0, cu_nodes[b+1] < cu_nodes[b] or
                                cu_nodes[b+1] > T: no call reads or writes any row
                                of the sequence (only status[b] is written) */
+  /* written by the paged-cache calls and tgdn_paged_tree_attention: */
+  TGDN_SEQ_BAD_PAGE = 8,    /* a page number outside the pool, a length beyond the
+                               held pages, an index outside the batch, or a fork
+                               onto a sequence that holds pages */
+  TGDN_SEQ_NO_PAGES = 9     /* not enough free pages, or table columns */
 } tgdn_seq_status;
 
 /* Element type of q, k, v and o.  g, b, S0, the state and the workspace are
  * always fp32. */
-typedef enum { TGDN_F32 = 0, TGDN_BF16 = 1 } tgdn_dtype;
+typedef enum {
+  TGDN_F32 = 0,
+  TGDN_BF16 = 1,
+  TGDN_F16 = 2 /* rotary positions, prompt and paged attention, paged cache only */
+} tgdn_dtype;
 
 /* Library limits. */
 #define TGDN_MAX_NODES 256  /* n_max bound: nodes per tree, root included */
@@ -329,6 +338,194 @@ int tgdn_verify_fused(const tgdn_tree* tree, const tgdn_dims* dims, const void* 
 int tgdn_verify_noalloc(const tgdn_tree* tree, const tgdn_dims* dims, const void* q,
                         const void* k, const void* v, const float* g, const float* b,
                         const float* S0, void* o, tgdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The verifier's attention layers around tgdn_tree_attention: rotary positions,
+ * attention over whole prompts, and a paged key/value cache with the tree
+ * attention that reads it (Problemstellung: the hybrid verifier's attention
+ * layers; the pages leave positions, prefill and the cache to the serving
+ * engine).
+ *
+ * Row strides.  q, k, v and o of these calls are [rows][heads][d] with the heads
+ * of a row contiguous and `stride` elements from one row to the next, so that
+ * views of one fused projection [rows][H_q + 2 H_kv][d] are taken as they are.
+ * ------------------------------------------------------------------------ */
+
+/* How tgdn_rope_freqs stretches the frequencies theta^(-2i/rot), i = 0 .. rot/2 - 1,
+ * for contexts longer than the trained one. */
+typedef enum {
+  TGDN_ROPE_NONE = 0,
+  TGDN_ROPE_LINEAR = 1, /* every frequency divided by `factor` (position interpolation) */
+  TGDN_ROPE_NTK = 2,    /* theta raised to theta * factor^(rot / (rot - 2)) */
+  TGDN_ROPE_YARN = 3    /* pairs that turn more than beta_fast times within orig_len
+                           positions kept, those that turn less than beta_slow times
+                           divided by `factor`, a linear ramp over the pair index
+                           between; the rotated values scaled by 0.1 ln(factor) + 1 */
+} tgdn_rope_scaling;
+
+/* HOST call: fills freq[rot / 2] (host memory) with each pair's turns per position
+ * as a 64-bit binary fraction, round(2^64 f_i / (2 pi)) mod 2^64, and *mscale with the
+ * factor on the rotated values.  Position times fraction then wraps at whole turns
+ * without error, so far positions keep their phase.  rot even, 2 .. 256 (4 at least for
+ * TGDN_ROPE_NTK); theta > 1; factor >= 1 and finite; for TGDN_ROPE_YARN orig_len >= 1
+ * and beta_fast > beta_slow > 0.  Returns TGDN_OK, TGDN_EINVAL or TGDN_ETOOBIG. */
+#define TGDN_ROPE_MAX_DIM 256
+int tgdn_rope_freqs(int32_t rot, double theta, int32_t scaling, double factor,
+                    int32_t orig_len, double beta_fast, double beta_slow, uint64_t* freq,
+                    float* mscale);
+
+/* Rotary positions of q and k: in the first `rot` elements of every head, pair i,
+ * (x_i, x_{i + rot/2}), or (x_{2i}, x_{2i+1}) with interleaved != 0, is turned by
+ * p f_i and scaled by mscale:  (x, y) -> mscale (x cos - y sin, x sin + y cos).  With
+ * transpose != 0 the turn is by -p f_i: the gradient of the call with respect to its
+ * inputs.  The remaining d - rot elements are copied.
+ * Position of row t of sequence b (cu[b] <= t < cu[b+1]):
+ *   p = (base ? base[b] : 0) + (off ? off[t] : t - cu[b])
+ * e.g. base = cached lengths with off = a draft tree's depths, or neither for whole
+ * prompts.  Rows outside every sequence are not written; neither are those of a
+ * sequence whose range leaves [0, T).
+ *   cu    [B + 1] int32, non-decreasing;  base [B], off [T] int32, may be NULL
+ *   freq  [rot / 2] uint64 (device), from tgdn_rope_freqs
+ *   q, q_out [T][H_q][d], k, k_out [T][H_kv][d] of io dtype (f32, bf16 or f16); an
+ *         output may be its own input (in place), not a shifted overlap of it
+ * d a multiple of 8, 8 .. 256; rot even, 2 .. d; strides multiples of 8 elements and at
+ * least heads * d; rows 16-byte aligned.  H_kv may be 0 (k, k_out NULL).
+ * The angle's cosine and sine are formed in fp32 from the exact phase; products in fp32,
+ * rounded once.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
+int tgdn_rope(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d, int32_t rot,
+              int32_t interleaved, int32_t transpose, int32_t io, float mscale,
+              const uint64_t* freq, const int32_t* cu, const int32_t* base,
+              const int32_t* off, const void* q, int64_t q_stride, const void* k,
+              int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+              int64_t k_out_stride, tgdn_stream_t stream);
+
+/* Causal attention over whole prompts, packed one after another: row t of sequence b
+ * (cu[b] <= t < cu[b+1]) attends to rows cu[b] .. t,
+ *   o[t][h] = softmax_j(scale * q[t][h] . k_j) v_j,
+ * query head h reading key/value head h / (H_q / H_kv).
+ *   cu     [B + 1] int32 (device); a sequence whose range leaves [0, T) is skipped
+ *   q, o   [T][H_q][d], k, v [T][H_kv][d] of io dtype (bf16 or f16); o overlaps no input
+ *   status [B] int32, written: TGDN_SEQ_OK, _BAD_RANGE or _TIMEOUT
+ *   ws     tgdn_prompt_attention_workspace_bytes() bytes (may be NULL when that is 0)
+ * A value that only masked positions hold, NaN and infinities included, reaches no row.
+ * d a multiple of 8, 8 .. 128; H_q / H_kv a whole number, at most 128; strides multiples
+ * of 8 elements and at least heads * d; pointers 16-byte aligned; scale positive and
+ * finite.  Scores, softmax statistics and sums are fp32; the probabilities enter the
+ * second product rounded to the io type.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG,
+ * TGDN_EUNSUPPORTED or TGDN_ECUDA. */
+int tgdn_prompt_attention(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d,
+                          int32_t io, const int32_t* cu, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          float scale, void* o, int64_t o_stride, int32_t* status, void* ws,
+                          size_t ws_bytes, tgdn_stream_t stream);
+size_t tgdn_prompt_attention_workspace_bytes(int32_t B, int32_t T, int32_t H_q, int32_t H_kv,
+                                             int32_t d);
+
+/* Bookkeeping of a paged key/value cache (device arrays owned by the caller), shared by
+ * all attention layers.  Position p of sequence b lies in page table[b][p / page_size].
+ *   B          rows of the table (sequences)
+ *   n_pages    pages of the pool; page_size positions per page: 16, 32, 64, 128 or 256
+ *   max_pages  columns of the table
+ *   table  [B][max_pages] int32;  columns past held[b] keep what they had
+ *   len    [B] cached positions, 0 .. held * page_size
+ *   held   [B] pages in the table row, 0 .. max_pages
+ *   refs   [n_pages] table entries that name the page; 0: free
+ *   status [B] written by the page calls for the sequences they handle (tgdn_seq_status)
+ * A fresh cache is len = held = refs = 0.  Pages shared between sequences are full ones;
+ * the page a sequence writes into is its own.  Free pages are always taken lowest number
+ * first, so the same calls give the same tables.  The page calls of one cache are ordered
+ * on one stream; a sequence with an error is left as it was.
+ *
+ * A layer's pages: keys [n_pages][H_kv][page_size][d] and values likewise.  The pool of
+ * `layers` layers is [layers][2 (keys, values)][n_pages][H_kv][page_size][d] of 2-byte
+ * elements (bf16 or f16), 16-byte aligned, d a multiple of 8, 8 .. 256. */
+typedef struct {
+  int32_t B, n_pages, page_size, max_pages;
+  int32_t* table;
+  int32_t* len;
+  int32_t* held;
+  int32_t* refs;
+  int32_t* status;
+} tgdn_pages;
+typedef struct {
+  int32_t layers, H_kv, d;
+  void* data;
+} tgdn_pool;
+
+/* Bytes of the workspace of the page calls (256-byte aligned); 0 for invalid arguments. */
+size_t tgdn_pages_workspace_bytes(const tgdn_pages* pages);
+
+/* Gives every sequence b the pages that len[b] + add[b] positions need.  Sequences are
+ * served in order: b gets its pages if the table has the columns and those asked for by
+ * sequences 0 .. b with enough columns do not exceed the free pages; otherwise it gets
+ * none (TGDN_SEQ_NO_PAGES).  A negative add or inconsistent len / held:
+ * TGDN_SEQ_BAD_PAGE.  Returns TGDN_OK, TGDN_EINVAL or TGDN_ECUDA. */
+int tgdn_pages_reserve(const tgdn_pages* pages, const int32_t* add, void* ws,
+                       tgdn_stream_t stream);
+
+/* Writes new keys and values at positions len[b], len[b] + 1, ... of every layer, the
+ * pages reserved before.  Without `path` (NULL) sequence b's new rows are cu[b] ..
+ * cu[b+1] - 1 (a prompt); with it they are cu[b] + path[b][i], i < n_path[b] (the
+ * accepted path of a draft tree: tgdn_accept's path and accept_len).
+ *   k, v  [layers][T][H_kv][d]: `row` elements between rows (a multiple of 8, at least
+ *         H_kv * d), `layer` elements between layers (a multiple of 8)
+ * With advance != 0 len[b] then grows by the rows written; without it the lengths stay
+ * (layers appended one by one, the last call advancing).  A sequence whose rows leave
+ * [cu[b], cu[b+1]) or [0, T), or do not fit its pages, is not written
+ * (TGDN_SEQ_BAD_RANGE, TGDN_SEQ_NO_PAGES or TGDN_SEQ_BAD_PAGE).  path_len is path's
+ * second dimension.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
+int tgdn_pages_append(const tgdn_pages* pages, const tgdn_pool* pool, int32_t T,
+                      const int32_t* cu, const int32_t* path, int32_t path_len,
+                      const int32_t* n_path, const void* k, int64_t k_layer, int64_t k_row,
+                      const void* v, int64_t v_layer, int64_t v_row, int32_t advance,
+                      tgdn_stream_t stream);
+
+/* Makes sequence dst[i] a copy of src[i] for i < n, all sources as they were before the
+ * call: full pages are shared, a partly filled last page is copied in every layer (its
+ * filled positions).  dst[i] must hold no pages and appear once.  status[i] per fork:
+ * TGDN_SEQ_OK, TGDN_SEQ_BAD_PAGE (indices, a target in use, an inconsistent source) or
+ * TGDN_SEQ_NO_PAGES (forks are served in order, as in tgdn_pages_reserve).
+ * n <= TGDN_PAGES_MAX_LIST.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
+#define TGDN_PAGES_MAX_LIST 4096
+int tgdn_pages_fork(const tgdn_pages* pages, const tgdn_pool* pool, int32_t n,
+                    const int32_t* src, const int32_t* dst, int32_t* status, void* ws,
+                    tgdn_stream_t stream);
+
+/* Releases every page of sequences seq[0 .. n-1] (len = held = 0); a page that no other
+ * sequence names becomes free.  Indices outside [0, B) are passed over, repeated ones
+ * release once.  Returns TGDN_OK, TGDN_EINVAL or TGDN_ECUDA. */
+int tgdn_pages_free(const tgdn_pages* pages, int32_t n, const int32_t* seq,
+                    tgdn_stream_t stream);
+
+/* Moves the live pages together: with n_live pages in use, the i-th page in use from
+ * n_live on moves to the i-th free page below it, in every layer, and the tables follow.
+ * Afterwards pages n_live .. n_pages - 1 are free.  *n_live (device int32) is written.
+ * Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
+int tgdn_pages_compact(const tgdn_pages* pages, const tgdn_pool* pool, int32_t* n_live,
+                       void* ws, tgdn_stream_t stream);
+
+/* tgdn_tree_attention over a paged cache: node n of sequence b attends to the cached
+ * positions 0 .. pages->len[b] - 1 and to the nodes on its own root path, itself included.
+ * One-node trees are plain decoding of single tokens.
+ *   q, o    [T][H_q][d];  k_tree, v_tree [T][H_kv][d] (the tree's own rows)
+ *   k_pages, v_pages [n_pages][H_kv][page_size][d] (one layer)
+ *   ws      optional workspace of tgdn_paged_tree_attention_workspace_bytes() bytes, 256-byte
+ *           aligned (NULL or fewer bytes: no item's keys are split over CTAs)
+ * all of io dtype (bf16 or f16).  tree->B must equal pages->B; tgdn_tree_prep must have run
+ * on `tree`.  Sequences with a bad status get zero outputs; one with a page number outside
+ * the pool or a length beyond its pages gets TGDN_SEQ_BAD_PAGE in tree->status and zeros.
+ * A value that only masked positions hold, NaN and infinities included, reaches no row;
+ * neither do the positions of a page past len[b].  n_max up to TGDN_MAX_NODES; other limits
+ * and precision as tgdn_prompt_attention.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG,
+ * TGDN_EUNSUPPORTED or TGDN_ECUDA. */
+int tgdn_paged_tree_attention(const tgdn_tree* tree, const tgdn_pages* pages, int32_t H_q,
+                              int32_t H_kv, int32_t d, int32_t io, const void* q,
+                              int64_t q_stride, const void* k_tree, int64_t k_stride,
+                              const void* v_tree, int64_t v_stride, const void* k_pages,
+                              const void* v_pages, float scale, void* o, int64_t o_stride,
+                              void* ws, size_t ws_bytes, tgdn_stream_t stream);
+size_t tgdn_paged_tree_attention_workspace_bytes(const tgdn_tree* tree, int32_t H_q,
+                                                 int32_t H_kv, int32_t d);
 
 /* Test hook for the bounded device waits; the paper has no counterpart and it is
  * not meant for production use.  Every device wait of the library gives up after

@@ -1,0 +1,703 @@
+// attn_core.cuh — the attention pipeline shared by the prompt kernel and the paged tree
+// kernel: o = softmax(scale q k^T) v over tiles of 128 keys, on 5th-generation tensor cores.
+//
+// A work item is (sequence, key/value head, block of query rows); a query row is
+// (token, query head of the group), row = token * G + g, so that all G = H_q / H_kv heads
+// that read a key/value head share its tiles.  A block holds two row tiles of 128 rows, and
+// every key and value tile is read once for both.  384 threads, one CTA per SM (TMEM):
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: one thread per row (= TMEM lane)
+//   warp 8          issues every tensor-core product
+//   warp 9          work list, tensor copies (TMA)
+//   warps 10, 11    value rows of partly visible tiles (below); outputs of invalid sequences
+// The roles run over the work list as one stream of key tiles: the next item's copies and
+// first score products go out while the current one finishes.
+//
+//   S_t = Q_t K^T   (tcgen05.mma, both operands in shared memory; 128 fp32 TMEM columns)
+//   P_t = 2^(c S_t - c m), c = scale log2(e)   (16-bit pairs over S_t's own columns)
+//   O_t += P_t V    (A from TMEM, V as the MN-major operand)
+// with a running row maximum m that moves (and rescales O_t and the sum) only when a tile
+// exceeds it by more than e^8: P stays below e^8, far inside fp16's range, and O and the
+// row sum stay in fp32.  While one tile's softmax runs, the tensor core works for the
+// other.  A 128-key step of both tiles (d = 128) is 32 instructions of 64 cycles, twice
+// the 1024 cycles that its 32,768 exponentials take, so the tensor core bounds it.
+//
+// Value rows that no row of the item may see.  A product cannot skip them: 0 x NaN is NaN.
+// Warps 10-11 therefore zero the rows past the visible keys of a tile (the end of a
+// sequence, stale positions of a page) before the product reads it, and in tiles where the
+// mask differs from row to row they replace non-finite values by zero and raise the item's
+// `dirty` flag; the epilogue then adds those values to just the rows that see them.
+//
+// Every wait is bounded; on expiry the sequence is marked TGDN_SEQ_TIMEOUT.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "launch_after.cuh"
+#include "tgdn_device.cuh"
+#include "tgdn_kernels.h"
+
+namespace tgdn {
+namespace attn {
+
+constexpr int kKeys = 128;   // keys per tile
+constexpr int kRows = 128;   // query rows per row tile
+constexpr int kBlock = 384;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kFixWarp = 10;
+constexpr int kRing = 4;     // work items known ahead
+constexpr int kFixRing = 4;  // value tiles being made safe (at most 4 value tiles are in flight)
+constexpr float kGap = 8.f;  // lazy rescaling threshold (natural log units)
+constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (128 each), O_0, O_1 (128 each)
+constexpr int kMaxNodes = TGDN_MAX_NODES;
+
+// Shared-memory layout for heads padded to DP = 64 or 128 elements.
+template <int DP>
+struct Lay {
+  static constexpr int kHalves = DP / 64;               // 128-byte swizzled halves of a row
+  static constexpr int kHalf = kKeys * 128;             // one half of a tile
+  static constexpr int kTile = kHalf * kHalves;         // a key, value or query tile
+  static constexpr int kStages = DP == 128 ? 5 : 8;     // key and value tiles in flight
+  static constexpr int kOffKV = 2 * kTile;              // (the two query tiles come first)
+  static constexpr int kOffMisc = kOffKV + kStages * kTile;
+};
+
+// One piece of work: key tiles [u0, u1) of an item.
+struct Seg {
+  int b, lo, N;      // sequence, its first row, its rows (tokens or nodes); b < 0: no more work
+  int tok0, hk;      // first token of row tile 0; key/value head
+  int e0, e1;        // row tile t takes tiles [u0, e_t); e_t <= u0: it has none
+  int u0, u1;
+  int P, npre;       // cached positions and their tiles (paged)
+  int part;          // -1: the whole item; else this CTA's partial-result slot
+  int zero;          // the sequence came with an error: its outputs are zeros
+};
+
+struct Args {
+  int B, T, H_q, H_kv, G, d, tpt;  // tpt: tokens per row tile = 128 / G
+  int gbox;                        // bytes of one half of a query box: 128 * G * tpt
+  float scale;
+  const int32_t* cu;
+  int32_t* status;
+  void* o;
+  int64_t o_stride;                // elements between tokens
+  const void* v;                   // new rows' values (prompt or tree), for the rare exact path
+  int64_t v_stride;
+  // paged
+  int n_max, words, ps, n_pages, max_pages;
+  const int32_t *order, *pos, *table, *len, *held;
+  const uint64_t* anc;
+  int tiles;                       // row tiles per item: 2, or 1 when items are few
+  float* part;                     // partial results (null: items are never split)
+  int4* desc;                      // [grid][2]: the split item that begins in a CTA's range
+  int part_rows;                   // rows per partial slot
+};
+
+// A partial row: O (DP), then the reference maximum in log2 units and the sum.
+template <int DP>
+constexpr int part_stride() { return DP + 4; }
+
+template <typename E> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr uint32_t kFmt = 1, kExp = 0x7f807f80u, kStep = 0x00800080u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
+};
+template <> struct Elem<__half> {
+  static constexpr uint32_t kFmt = 0, kExp = 0x7c007c00u, kStep = 0x04000400u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
+};
+
+// Instruction descriptor, fp32 accumulation; bf16 or fp16 operands of one type.
+__host__ __device__ constexpr uint32_t idesc(uint32_t fmt, int M, int N, int b_mn) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Until this thread's tensor-memory loads are complete; the operands keep every use of the
+// loaded registers behind the wait.
+__device__ __forceinline__ void ld_wait32(float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]),
+                 "+r"(u[6]), "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]),
+                 "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]), "+r"(u[16]), "+r"(u[17]),
+                 "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]),
+                 "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]),
+                 "+r"(u[30]), "+r"(u[31])
+               :
+               : "memory");
+}
+
+struct Bars {
+  uint64_t kvfull[8], kvempty[8];
+  uint64_t qfull, qempty, drain;
+  uint64_t sfull[2], pready[2], pvdone[2];
+  uint64_t fixed[kFixRing];
+  uint64_t segfull[kRing], segempty[kRing];
+  Seg seg[kRing];
+  int dirty[kRing], bad[kRing];
+  uint32_t tmem;
+  int abort;
+  int where;  // the sequence in work when a wait expired
+};
+
+template <int DP, bool PAGED>
+constexpr int smem_bytes() {
+  return Lay<DP>::kOffMisc + (int)sizeof(Bars) + (PAGED ? 4 * kMaxNodes : 0) + 1024;
+}
+static_assert(smem_bytes<128, true>() <= 227 * 1024, "fits one CTA per SM");
+
+// ------------------------------------------------------------------ masks and the rare path
+// Whether tile u needs the value check, its visible rows, and whether the mask differs by row.
+template <bool PAGED>
+__device__ __forceinline__ bool tile_part(const Seg& s, int u, int& lim, bool& by_row) {
+  if (PAGED) {
+    if (u < s.npre) {
+      lim = min(kKeys, s.P - u * kKeys);
+      by_row = false;
+      return lim < kKeys;
+    }
+    lim = min(kKeys, s.N - (u - s.npre) * kKeys);
+    by_row = s.N > 1;
+    return true;
+  }
+  lim = min(kKeys, s.N - u * kKeys);
+  by_row = u * kKeys + kKeys - 1 > s.tok0;
+  return by_row;
+}
+
+// Sum of the non-finite values of column `col` over the keys of partly visible tiles that
+// this row sees (mask words of the tree, or keys up to its own token).
+template <typename E, bool PAGED>
+__device__ __noinline__ float nonfinite_sum(const Args* a, const Seg* s, int tok,
+                                            const uint32_t* mask, int col) {
+  const E* v = static_cast<const E*>(a->v);
+  float sum = 0.f;
+  for (int u = s->u0; u < s->u1; ++u) {
+    int lim;
+    bool by_row;
+    if (!tile_part<PAGED>(*s, u, lim, by_row) || !by_row) continue;
+    const int k0 = (u - (PAGED ? s->npre : 0)) * kKeys;
+    for (int k = k0; k < k0 + lim; ++k) {
+      const bool seen = PAGED ? (mask[k >> 5] >> (k & 31)) & 1u : k <= tok;
+      if (!seen) continue;
+      const float x = Elem<E>::up(v[(int64_t)(s->lo + k) * a->v_stride + (int64_t)s->hk * a->d + col]);
+      if (!isfinite(x)) sum += x;
+    }
+  }
+  return sum;
+}
+
+// ------------------------------------------------------------------ the pipeline
+// W: the work list of this CTA; `bool next(Seg&)` is called by every lane of the copy warp.
+template <int DP, typename E, bool PAGED, typename W>
+__device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUtensorMap* qmap,
+                                         const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                         const CUtensorMap* kpmap, const CUtensorMap* vpmap) {
+  using L = Lay<DP>;
+  constexpr int NS = L::kStages;
+  Bars* br = reinterpret_cast<Bars*>(smem + L::kOffMisc);
+  uint8_t* sord = smem + L::kOffMisc + sizeof(Bars);  // [row tile][2][256] order bytes (paged)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&br->kvfull[i], 1);
+      mbar_init(&br->kvempty[i], 1);
+    }
+    mbar_init(&br->qfull, 1);
+    mbar_init(&br->qempty, 1);
+    mbar_init(&br->drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&br->sfull[i], 1);
+      mbar_init(&br->pready[i], 4);
+      mbar_init(&br->pvdone[i], 1);
+    }
+    for (int i = 0; i < kFixRing; ++i) mbar_init(&br->fixed[i], 2);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&br->segfull[i], 1);
+      mbar_init(&br->segempty[i], 1 + 8 + 2);
+    }
+    fence_mbar_init();
+    br->abort = 0;
+    br->where = -1;
+  }
+  if (warp == kMmaWarp) tmem_alloc(&br->tmem, kTmemCols);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  grid_dependency_wait();
+  const uint32_t tmem = br->tmem;
+  volatile int* abort = &br->abort;
+  bool ok = true;
+
+  if (warp == kCopyWarp) {
+    // ---------------- work list and copies
+    W work(a);
+    uint32_t cnt = 0;  // key and value tiles requested
+    int n_q = 0;       // items whose queries were requested
+    auto slot_free = [&](uint32_t c) -> bool {
+      return c < NS || mbar_wait_suspend(&br->kvempty[c % NS], ((c / NS) - 1) & 1, abort);
+    };
+    int n = 0;
+    Seg s;
+    for (; ok; ++n) {
+      const int r = n % kRing;
+      if (n >= kRing) ok = mbar_wait_suspend(&br->segempty[r], ((n / kRing) - 1) & 1, abort);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const bool more = work.next(s);
+      if (!more) s.b = -1;
+      if (lane == 0) {
+        br->seg[r] = s;
+        br->dirty[r] = 0;
+        br->bad[r] = 0;
+        mbar_arrive(&br->segfull[r]);
+      }
+      __syncwarp();
+      if (!more) break;
+      // page of this lane in tile u (lanes past the tile's pages, or a bad entry: -1)
+      const int ppt = PAGED ? max(1, kKeys / a.ps) : 1;
+      const int prow = PAGED ? min(a.ps, kKeys) : kKeys;
+      auto page_of = [&](int u) -> int {
+        if (!PAGED || u >= s.npre || lane >= ppt) return -1;
+        const int64_t at = (int64_t)u * kKeys + (int64_t)lane * a.ps;
+        if (at >= s.P) return -1;
+        return a.table[(int64_t)s.b * a.max_pages + at / a.ps];
+      };
+      int page = page_of(s.u0);
+      auto load = [&](int u, bool val, int pg) {
+        uint64_t* bar = &br->kvfull[cnt % NS];
+        uint8_t* dst = smem + L::kOffKV + (cnt % NS) * L::kTile;
+        if (PAGED && u < s.npre) {
+          const CUtensorMap* m = val ? vpmap : kpmap;
+          const int left = s.P - u * kKeys;
+          const int np = min(ppt, (left + a.ps - 1) / a.ps);
+          if (lane == 0) mbar_arrive_expect_tx(bar, np * prow * 128 * L::kHalves);
+          __syncwarp();
+          if (lane < np) {
+            const int in = a.ps > kKeys ? (u * kKeys) % a.ps : 0;
+            const int z = pg * a.H_kv + s.hk;
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+              tma_load_3d(dst + h * L::kHalf + lane * prow * 128, m, bar, h * 64, in, z);
+          }
+        } else if (lane == 0) {
+          const CUtensorMap* m = val ? vmap : kmap;
+          const int row = s.lo + (u - (PAGED ? s.npre : 0)) * kKeys;
+          mbar_arrive_expect_tx(bar, L::kTile);
+#pragma unroll
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_3d(dst + h * L::kHalf, m, bar, h * 64, s.hk, row);
+        }
+        __syncwarp();
+        ++cnt;
+      };
+      for (int u = s.u0; ok && u < s.u1; ++u) {
+        if (PAGED) {
+          const bool mine = u < s.npre && lane < ppt && (int64_t)u * kKeys + (int64_t)lane * a.ps < s.P;
+          const bool wrong = mine && (page < 0 || page >= a.n_pages);
+          if (__any_sync(0xffffffffu, wrong)) {
+            // a page outside the pool: nothing of it is read; the sequence gets zeros
+            if (wrong) page = 0;
+            if (lane == 0) {
+              br->bad[r] = 1;
+              atomicCAS(&a.status[s.b], TGDN_SEQ_OK, TGDN_SEQ_BAD_PAGE);
+            }
+            __syncwarp();
+          }
+        }
+        const int next_page = u + 1 < s.u1 ? page_of(u + 1) : -1;
+        ok = slot_free(cnt);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        load(u, false, page);
+        if (u == s.u0) {  // the queries, once the previous item's score products are done
+          if (n > 0) ok = mbar_wait_suspend(&br->qempty, (n - 1) & 1, abort);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          ++n_q;
+          if (lane == 0) {
+            const int tiles = s.e1 > s.u0 ? 2 : 1;
+            mbar_arrive_expect_tx(&br->qfull, tiles * a.gbox * L::kHalves);
+            for (int t = 0; t < tiles; ++t)
+#pragma unroll
+              for (int h = 0; h < L::kHalves; ++h)
+                tma_load_3d(smem + t * L::kTile + h * L::kHalf, qmap, &br->qfull, h * 64,
+                            s.hk * a.G, s.lo + s.tok0 + t * a.tpt);
+          }
+          __syncwarp();
+        }
+        ok = slot_free(cnt);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        load(u, true, page);
+        page = next_page;
+      }
+    }
+    if (!ok) {  // let the copies in flight land before the shared memory goes (bounded)
+      if (lane == 0) br->where = s.b;
+      for (uint32_t c = cnt > NS ? cnt - NS : 0; c < cnt; ++c)
+        (void)mbar_wait(&br->kvfull[c % NS], (c / NS) & 1);
+      if (n_q > 0) (void)mbar_wait(&br->qfull, (n_q - 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- products
+    if (lane == 0) {
+      uint32_t cnt = 0, fix = 0;    // tiles seen; value tiles made safe
+      uint32_t done[2] = {0, 0};    // steps of each row tile
+      constexpr uint32_t id_s = idesc(Elem<E>::kFmt, 128, kKeys, 0);
+      constexpr uint32_t id_o = idesc(Elem<E>::kFmt, 128, DP, 1);
+      const uint32_t sQ = smem_addr(smem), sKV = smem_addr(smem + L::kOffKV);
+      auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
+        // the previous O_t += P_t V has read P_t, which lies in S_t's columns
+        if (done[t] > 0 && !mbar_wait_suspend(&br->pvdone[t], (done[t] - 1) & 1, abort)) return false;
+        tc_fence_after_sync();
+        const uint32_t q = sQ + t * L::kTile, k = sKV + (c % NS) * L::kTile;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+          umma_bf16(tmem + t * 128,
+                    smem_desc(q + (i >> 2) * L::kHalf + (i & 3) * 32, 16, 1024, kSwizzle128B),
+                    smem_desc(k + (i >> 2) * L::kHalf + (i & 3) * 32, 16, 1024, kSwizzle128B), id_s,
+                    i > 0);
+        umma_commit(&br->sfull[t]);
+        return true;
+      };
+      auto pv = [&](int t, uint32_t c, bool first) {  // O_t (+)= P_t V of the tile in slot c
+        tc_fence_after_sync();
+        const uint32_t v = sKV + (c % NS) * L::kTile;
+#pragma unroll
+        for (int i = 0; i < kKeys / 16; ++i)
+          umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + i * 8,
+                           smem_desc(v + i * 2048, L::kHalf, 1024, kSwizzle128B), id_o,
+                           (!first || i > 0) ? 1u : 0u);
+        umma_commit(&br->pvdone[t]);
+      };
+      int n = 0;
+      for (; ok; ++n) {
+        const int r = n % kRing;
+        ok = mbar_wait_suspend(&br->segfull[r], (n / kRing) & 1, abort);
+        if (!ok) break;
+        const Seg s = br->seg[r];
+        if (s.b < 0) break;
+        ok = mbar_wait_suspend(&br->qfull, n & 1, abort) &&
+             mbar_wait_suspend(&br->kvfull[cnt % NS], (cnt / NS) & 1, abort);
+        const bool a0 = s.e0 > s.u0, a1 = s.e1 > s.u0;
+        if (ok && a0) ok = score(0, cnt);
+        if (ok && a1) ok = score(1, cnt);
+        if (ok) {
+          umma_commit(&br->kvempty[cnt % NS]);
+          if (s.u1 - s.u0 == 1) umma_commit(&br->qempty);
+        }
+        for (int u = s.u0; ok && u < s.u1; ++u) {
+          const uint32_t cv = cnt + 1, ck = cnt + 2;  // this value tile, the next key tile
+          const bool x0 = u < s.e0, x1 = u < s.e1;    // steps of the row tiles
+          const bool y0 = u + 1 < s.e0, y1 = u + 1 < s.e1;
+          bool pv1 = !x1;
+          if (x0) ok = mbar_wait_suspend(&br->pready[0], done[0] & 1, abort);
+          if (ok) ok = mbar_wait_suspend(&br->kvfull[cv % NS], (cv / NS) & 1, abort);
+          int lim;
+          bool by_row;
+          if (ok && tile_part<PAGED>(s, u, lim, by_row)) {
+            ok = mbar_wait_suspend(&br->fixed[fix % kFixRing], (fix / kFixRing) & 1, abort);
+            ++fix;
+          }
+          if (!ok) break;
+          if (x0) {
+            pv(0, cv, u == s.u0);
+            ++done[0];
+          }
+          // the other tile's product first if its P is there already: S_0 has to wait for
+          // the product just issued
+          if (!pv1 && mbar_try(&br->pready[1], done[1] & 1)) {
+            pv(1, cv, u == s.u0);
+            ++done[1];
+            pv1 = true;
+          }
+          if (y0) ok = mbar_wait_suspend(&br->kvfull[ck % NS], (ck / NS) & 1, abort) && score(0, ck);
+          if (ok && !pv1) {
+            ok = mbar_wait_suspend(&br->pready[1], done[1] & 1, abort);
+            if (ok) {
+              pv(1, cv, u == s.u0);
+              ++done[1];
+            }
+          }
+          if (!ok) break;
+          umma_commit(&br->kvempty[cv % NS]);
+          if (y1) ok = mbar_wait_suspend(&br->kvfull[ck % NS], (ck / NS) & 1, abort) && score(1, ck);
+          if (ok && u + 1 < s.u1) {
+            umma_commit(&br->kvempty[ck % NS]);
+            if (u + 2 == s.u1) umma_commit(&br->qempty);
+          }
+          cnt += 2;
+        }
+        if (!ok) {
+          br->where = s.b;
+          break;
+        }
+        mbar_arrive(&br->segempty[r]);
+      }
+      // every product and every arrival it owes is done before the shared memory goes
+      umma_commit(&br->drain);
+      (void)mbar_wait(&br->drain, 0);
+    }
+    __syncwarp();
+  } else if (warp >= kFixWarp) {
+    // ---------------- value rows that must not reach the product
+    const int ft = tid - kFixWarp * 32;  // 0 .. 63
+    W::first(a, ft);  // status words, outputs of sequences that have no work
+    uint32_t cnt = 0, fix = 0;
+    for (int n = 0; ok; ++n) {
+      const int r = n % kRing;
+      ok = mbar_wait_suspend(&br->segfull[r], (n / kRing) & 1, abort);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const Seg s = br->seg[r];
+      if (s.b < 0) break;
+      for (int u = s.u0; ok && u < s.u1; ++u, cnt += 2) {
+        // every tile is awaited in turn, also those left alone: a barrier two phases back
+        // would pass for done
+        const uint32_t cv = cnt + 1;
+        ok = mbar_wait_suspend(&br->kvfull[cnt % NS], (cnt / NS) & 1, abort) &&
+             mbar_wait_suspend(&br->kvfull[cv % NS], (cv / NS) & 1, abort);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        int lim;
+        bool by_row;
+        if (!tile_part<PAGED>(s, u, lim, by_row)) continue;
+        uint4* tile = reinterpret_cast<uint4*>(smem + L::kOffKV + (cv % NS) * L::kTile);
+        uint32_t acc = 0;
+        for (int i = ft; i < L::kTile / 16; i += 64) {
+          const int row = (i >> 3) & (kKeys - 1);
+          if (row >= lim) {
+            tile[i] = make_uint4(0, 0, 0, 0);
+          } else if (by_row) {
+            const uint4 w = tile[i];
+            acc |= ((w.x & Elem<E>::kExp) + Elem<E>::kStep) | ((w.y & Elem<E>::kExp) + Elem<E>::kStep) |
+                   ((w.z & Elem<E>::kExp) + Elem<E>::kStep) | ((w.w & Elem<E>::kExp) + Elem<E>::kStep);
+          }
+        }
+        if (acc & 0x80008000u) {  // a non-finite value among this thread's
+          br->dirty[r] = 1;
+          uint32_t* w32 = reinterpret_cast<uint32_t*>(tile);
+          for (int i = ft; i < L::kTile / 16; i += 64)
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w = w32[i * 4 + j];
+              const uint32_t top = ((w & Elem<E>::kExp) + Elem<E>::kStep) & 0x80008000u;
+              if (top & 0x8000u) w &= 0xffff0000u;
+              if (top & 0x80000000u) w &= 0x0000ffffu;
+              w32[i * 4 + j] = w;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br->fixed[fix % kFixRing]);
+        ++fix;
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&br->segempty[r]);
+    }
+  } else {
+    // ---------------- softmax: row tile t, one row per thread
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + 256 + t * 128 + lanes;
+    const float c2 = a.scale * 1.4426950408889634f;
+    const float gap = kGap / a.scale;
+    const int tok_in = row / a.G, g = row - tok_in * a.G;
+    uint32_t done = 0, built = 0;
+    for (int n = 0; ok; ++n) {
+      const int r = n % kRing;
+      ok = mbar_wait_suspend(&br->segfull[r], (n / kRing) & 1, abort);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const Seg s = br->seg[r];
+      if (s.b < 0) break;
+      const int e = t == 0 ? s.e0 : s.e1;
+      if (e > s.u0) {
+        const int tok = s.tok0 + t * a.tpt + tok_in;
+        const bool live = tok_in < a.tpt && tok < s.N;
+        uint32_t mask[kMaxNodes / 32];  // (paged)
+        if constexpr (PAGED) {
+          // ancestor-or-self set in node-index space, from the topological order (staged as
+          // bytes) and the mask of the node's position; only where the tree's tiles come
+#pragma unroll
+          for (int w = 0; w < kMaxNodes / 32; ++w) mask[w] = 0;
+          if (e > s.npre) {
+            // every warp writes the whole copy (the same bytes), so none waits for another;
+            // two copies in turn: a warp gets to the copy after next only past products that
+            // all four warps fed
+            uint8_t* ord = sord + (t * 2 + (built & 1)) * kMaxNodes;
+            ++built;
+            for (int i = lane; i < s.N; i += 32) ord[i] = (uint8_t)a.order[s.lo + i];
+            __syncwarp();
+            const int p = live ? a.pos[s.lo + tok] : -1;
+            if (p >= 0 && p < s.N) {
+              for (int w = 0; w < a.words; ++w) {
+                uint64_t bits = a.anc[(int64_t)(s.lo + p) * a.words + w];
+                while (bits) {
+                  const int bp = w * 64 + __ffsll(static_cast<long long>(bits)) - 1;
+                  bits &= bits - 1;
+                  if (bp >= s.N) break;
+                  const int x = ord[bp];
+#pragma unroll
+                  for (int j = 0; j < kMaxNodes / 32; ++j)
+                    if ((x >> 5) == j) mask[j] |= 1u << (x & 31);
+                }
+              }
+            }
+          }
+        }
+        float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int u = s.u0; u < e; ++u) {
+          ok = mbar_wait_suspend(&br->sfull[t], done & 1, abort);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after_sync();
+          float x[kKeys];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, reinterpret_cast<float(&)[32]>(x[q * 32]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ld_wait32(x + q * 32);
+          // masks
+          if constexpr (PAGED) {
+            if (u >= s.npre) {
+              const int w0 = (u - s.npre) * 4;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t w = w0 == 0 ? mask[q] : mask[4 + q];
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!((w >> c) & 1u)) x[q * 32 + c] = -INFINITY;
+              }
+            } else if (s.P - u * kKeys < kKeys) {
+              const int lim = s.P - u * kKeys;
+#pragma unroll
+              for (int c = 0; c < kKeys; ++c)
+                if (c >= lim) x[c] = -INFINITY;
+            }
+          } else if (u * kKeys + kKeys - 1 > s.tok0) {
+            const int lim = live ? tok - u * kKeys : -1;
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              if (c > lim) x[c] = -INFINITY;
+          }
+          float mx[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            mx[c] = fmaxf(fmaxf(x[c], x[c + 32]), fmaxf(x[c + 64], x[c + 96]));
+#pragma unroll
+          for (int w = 16; w >= 1; w /= 2)
+#pragma unroll
+            for (int c = 0; c < w; ++c) mx[c] = fmaxf(mx[c], mx[c + w]);
+          const bool need = live && mx[0] > m + gap;  // also the first finite maximum
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha =
+                need ? (m == -INFINITY ? 0.f : fast_exp2((m - mx[0]) * c2)) : 1.f;
+            if (need) m = mx[0];
+            l0 *= alpha;
+            l1 *= alpha;
+            if (u > s.u0) {  // (the last product on O_t was done before S_t was issued)
+#pragma unroll 1
+              for (int q = 0; q < DP / 16; ++q) {
+                float o[16];
+                uint32_t w[16];
+                tmem_ld16(tO + q * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) w[c] = __float_as_uint(o[c] * alpha);
+                tmem_st16(tO + q * 16, w);
+              }
+            }
+          }
+          const float mc = m == -INFINITY ? 0.f : m * c2;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float p0 = fast_exp2(fmaf(x[q * 32 + 2 * c], c2, -mc));
+              const float p1 = fast_exp2(fmaf(x[q * 32 + 2 * c + 1], c2, -mc));
+              l0 += p0;
+              l1 += p1;
+              w[c] = Elem<E>::pack(p0, p1);
+            }
+            tmem_st16(tS + q * 16, w);
+          }
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&br->pready[t]);
+          ++done;
+        }
+        // the item's last product on O_t
+        if (ok) ok = mbar_wait_suspend(&br->pvdone[t], (done - 1) & 1, abort);
+        if (!(ok = __all_sync(0xffffffffu, ok))) {
+          if (lane == 0) br->where = s.b;
+          break;
+        }
+        tc_fence_after_sync();
+        const bool dirty = *reinterpret_cast<volatile int*>(&br->dirty[r]) != 0;
+        const bool bad = PAGED && (s.zero || *reinterpret_cast<volatile int*>(&br->bad[r]) != 0);
+        const float l = l0 + l1;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        E* orow = static_cast<E*>(a.o) + (int64_t)(s.lo + tok) * a.o_stride +
+                  (int64_t)(s.hk * a.G + g) * a.d;
+        float* prow = nullptr;
+        if (PAGED && s.part >= 0 && live)
+          prow = a.part + ((int64_t)(blockIdx.x * 2 + s.part) * a.part_rows + t * kRows + row) *
+                              part_stride<DP>();
+#pragma unroll 1
+        for (int q = 0; q < DP / 16; ++q) {
+          float o[16];
+          tmem_ld16(tO + q * 16, o);
+          tmem_ld_wait();
+          if (dirty && live) {
+            uint32_t seen[kMaxNodes / 32];
+#pragma unroll
+            for (int w = 0; w < kMaxNodes / 32; ++w) seen[w] = PAGED ? mask[w] : 0;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (q * 16 + c < a.d)
+                o[c] += nonfinite_sum<E, PAGED>(&a, &br->seg[r], tok, seen, q * 16 + c);
+          }
+          if (!live) continue;
+          if (prow != nullptr) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<float4*>(prow + q * 16 + c * 4) =
+                  make_float4(o[c * 4], o[c * 4 + 1], o[c * 4 + 2], o[c * 4 + 3]);
+          } else {
+            const float f = bad ? 0.f : inv;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (q * 16 + c * 8 >= a.d) continue;
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = bad ? 0u : Elem<E>::pack(o[c * 8 + 2 * i] * f, o[c * 8 + 2 * i + 1] * f);
+              *reinterpret_cast<uint4*>(orow + q * 16 + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (prow != nullptr) {
+          prow[DP] = m == -INFINITY ? 0.f : m * c2;
+          prow[DP + 1] = l;
+        }
+        tc_fence_before_sync();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br->segempty[r]);
+    }
+  }
+  // ---------------- teardown
+  tc_fence_before_sync();
+  const bool all_ok = __syncthreads_and(ok) != 0;
+  if (!all_ok && tid == 0 && br->where >= 0)
+    atomicCAS(&a.status[br->where], TGDN_SEQ_OK, TGDN_SEQ_TIMEOUT);
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace attn
+}  // namespace tgdn

@@ -1,0 +1,302 @@
+// paged_attn.cu — ancestor-masked tree attention over a paged key/value cache.
+//
+// Node n of sequence b attends to the cached positions 0 .. len[b] - 1, which lie in the
+// pages of its table row, and to the tree nodes on its own root path, itself included;
+// a one-node tree is plain single-token decoding.  The pipeline of attn_core.cuh, a key
+// tile being 128 / page_size page boxes of cached positions, then the tree's own rows.
+//
+// Decoding reads each cached key and value once for a handful of query rows, so memory
+// bounds it, and what costs is uneven lengths.  All key tiles of all items are therefore
+// numbered through and every CTA takes an equal run of them, wherever it begins and ends
+// (kMinShare at least: a cut costs a merge).  A run covers whole items and at most two
+// cut ones; the parts of a cut item (O unnormalised, reference maximum, sum) go to the
+// workspace and paged_merge_kernel joins them in order of their keys, so results do not
+// depend on timing.  Without a workspace items stay whole.
+#include "attn_core.cuh"
+
+namespace tgdn {
+namespace attn {
+
+constexpr int kMinShare = 4;  // key tiles per CTA below which a cut costs more than it saves
+
+// Cached and tree key tiles of sequence b; 0: no work (empty, or an error).
+struct Plan {
+  int lo, N, P, npre, nt, st;
+};
+__device__ __forceinline__ Plan plan_of(const Args& a, int b) {
+  Plan p{};
+  p.lo = a.cu[b];
+  const int hi = a.cu[b + 1];
+  p.st = a.status[b];
+  p.P = a.len[b];
+  const int held = a.held[b];
+  p.N = hi - p.lo;
+  // (words this kernel itself may write count as planned: every CTA plans the same work)
+  const bool run = p.st == TGDN_SEQ_OK || p.st == TGDN_SEQ_TIMEOUT || p.st == TGDN_SEQ_BAD_PAGE;
+  if (!run || p.lo < 0 || p.N <= 0 || hi > a.T || p.N > a.n_max || p.P < 0 || held < 0 ||
+      held > a.max_pages || p.P > (int64_t)held * a.ps)
+    return p;  // nt = 0
+  p.npre = (p.P + kKeys - 1) / kKeys;
+  p.nt = p.npre + (p.N + kKeys - 1) / kKeys;
+  return p;
+}
+__device__ __forceinline__ int64_t items_of(const Args& a, const Plan& p) {
+  const int blk = a.tpt * 2;
+  return p.nt ? (int64_t)((p.N + blk - 1) / blk) * a.H_kv : 0;
+}
+
+__device__ __forceinline__ int64_t warp_sum_upto(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+struct PagedWork {
+  const Args& a;
+  int lane, chunk = 0, n = 0;
+  int64_t before = 0, x, x1, share;
+  int4 d0, d1;
+
+  __device__ explicit PagedWork(const Args& args) : a(args), lane(threadIdx.x & 31) {
+    int64_t sum = 0;
+    for (int b = lane; b < a.B; b += 32) {
+      const Plan p = plan_of(a, b);
+      sum += items_of(a, p) * p.nt;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    share = (sum + gridDim.x - 1) / gridDim.x;
+    if (share < kMinShare) share = kMinShare;
+    x = min(sum, share * blockIdx.x);
+    x1 = min(sum, x + share);
+    d0 = make_int4(-1, 0, 0, 0);
+    d1 = make_int4(0, 0, 0, 0);
+  }
+
+  // Sequences without work but with rows: zeros, and the word for a bad length.
+  static __device__ void first(const Args& a, int ft) {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      const Plan p = plan_of(a, b);
+      if (p.nt || p.N <= 0 || p.st == TGDN_SEQ_BAD_RANGE || p.lo < 0 || p.lo + p.N > a.T) continue;
+      const int v8 = a.H_q * a.d / 8;  // 16-byte pieces of a row
+      for (int64_t i = ft; i < (int64_t)p.N * v8; i += 64)
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + (p.lo + i / v8) * a.o_stride)[i % v8] =
+            make_uint4(0, 0, 0, 0);
+      if (ft == 0) atomicCAS(&a.status[b], TGDN_SEQ_OK, TGDN_SEQ_BAD_PAGE);
+    }
+  }
+
+  __device__ bool next(Seg& s) {
+    while (x < x1) {
+      for (;; chunk += 32) {
+        Plan p{};
+        if (chunk + lane < a.B) p = plan_of(a, chunk + lane);
+        const int64_t tiles = items_of(a, p) * p.nt;
+        const int64_t upto = warp_sum_upto(tiles, lane);
+        const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+        if (x >= before + total) {
+          before += total;
+          continue;
+        }
+        const int64_t at = x - before;
+        const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+        const int64_t in = at - __shfl_sync(0xffffffffu, upto - tiles, f);
+        s.b = chunk + f;
+        s.lo = __shfl_sync(0xffffffffu, p.lo, f);
+        s.N = __shfl_sync(0xffffffffu, p.N, f);
+        s.P = __shfl_sync(0xffffffffu, p.P, f);
+        s.npre = __shfl_sync(0xffffffffu, p.npre, f);
+        const int nt = __shfl_sync(0xffffffffu, p.nt, f);
+        s.zero = __shfl_sync(0xffffffffu, p.st, f) != TGDN_SEQ_OK;
+        const int item = (int)(in / nt);
+        s.hk = item % a.H_kv;
+        s.tok0 = item / a.H_kv * a.tpt * 2;
+        s.u0 = (int)(in % nt);
+        const int64_t x_item = x - s.u0;
+        if (a.part == nullptr) {
+          x = x_item + nt;
+          if (s.u0 > 0) break;  // another CTA's
+          s.u1 = nt;
+        } else {
+          s.u1 = (int)min((int64_t)nt, s.u0 + (x1 - x));
+          x += s.u1 - s.u0;
+        }
+        s.part = s.u0 == 0 && s.u1 == nt ? -1 : (n == 0 ? 0 : 1);
+        s.e0 = s.u1;
+        s.e1 = s.tok0 + a.tpt < s.N ? s.u1 : 0;
+        if (s.u0 == 0 && s.u1 < nt) {
+          d0 = make_int4(s.b, s.lo, s.N, s.tok0);
+          d1 = make_int4(s.hk, (int)((x_item + nt - 1) / share), s.part, 0);
+        }
+        ++n;
+        return true;
+      }
+    }
+    if (a.part != nullptr && lane == 0) {
+      a.desc[2 * blockIdx.x] = d0;
+      a.desc[2 * blockIdx.x + 1] = d1;
+    }
+    return false;
+  }
+};
+
+template <int DP, typename E>
+__global__ void __launch_bounds__(kBlock, 1)
+paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap kpmap,
+                  const __grid_constant__ CUtensorMap vpmap, const __grid_constant__ Args a) {
+  extern __shared__ uint8_t pg_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(pg_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  pipeline<DP, E, true, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.x's run and goes on into later
+// ones: a warp per query row.
+//   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
+template <int DP, typename E>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ Args a) {
+  grid_dependency_wait();
+  const int c = blockIdx.x;
+  const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
+  if (d0.x < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (r >= a.part_rows) return;
+  const int t = r / kRows, row = r % kRows, tok_in = row / a.G;
+  const int tok = d0.w + t * a.tpt + tok_in;
+  if (tok_in >= a.tpt || tok >= d0.z) return;
+  constexpr int V = DP / 32;  // columns per lane
+  const int64_t slot = (int64_t)a.part_rows * part_stride<DP>();
+  const float* own = a.part + (2 * c + d1.z) * slot + (int64_t)r * part_stride<DP>();
+  const float* rest = a.part + (int64_t)r * part_stride<DP>();
+  auto row_of = [&](int i) { return i == c ? own : rest + 2 * i * slot; };
+  float M = -INFINITY;
+  for (int i = c + lane; i <= d1.y; i += 32) {
+    const float* p = row_of(i);
+    if (p[DP + 1] != 0.f) M = fmaxf(M, p[DP]);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float sum = 0.f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 4
+  for (int i = c; i <= d1.y; ++i) {
+    const float* p = row_of(i);
+    const float l = p[DP + 1];
+    const float w = l == 0.f ? 0.f : fast_exp2(p[DP] - M);
+    sum = fmaf(w, l, sum);
+    float x[V];
+    if (V == 4) {
+      const float4 y = reinterpret_cast<const float4*>(p)[lane];
+      x[0] = y.x, x[1] = y.y, x[V - 2] = y.z, x[V - 1] = y.w;
+    } else {
+      const float2 y = reinterpret_cast<const float2*>(p)[lane];
+      x[0] = y.x, x[1] = y.y;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[v], acc[v]);
+  }
+  const bool ok = a.status[d0.x] == TGDN_SEQ_OK;
+  const float inv = !ok || sum == 0.f ? 0.f : 1.f / sum;
+  if (lane * V >= a.d) return;
+  E* orow = static_cast<E*>(a.o) + (int64_t)(d0.y + tok) * a.o_stride +
+            (int64_t)(d1.x * a.G + row % a.G) * a.d + lane * V;
+  uint32_t w[2];
+#pragma unroll
+  for (int v = 0; v < V / 2; ++v)
+    w[v] = ok ? Elem<E>::pack(acc[2 * v] * inv, acc[2 * v + 1] * inv) : 0u;
+  if (V == 4)
+    *reinterpret_cast<uint2*>(orow) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(orow) = w[0];
+}
+
+struct Split {
+  int grid, rows;
+  size_t part_off, bytes;
+};
+static Split split_of(int n_max, int G, int d) {
+  Split p;
+  const int dp = d > 64 ? 128 : 64, tpt = kRows / G;
+  p.grid = device_sm_count();
+  p.rows = n_max <= tpt ? n_max * G : 2 * kRows;
+  p.part_off = ((size_t)p.grid * 2 * sizeof(int4) + 255) / 256 * 256;
+  p.bytes = p.part_off + (size_t)p.grid * 2 * p.rows * (dp + 4) * sizeof(float);
+  return p;
+}
+
+template <int DP, typename E>
+static cudaError_t launch(const Args& a, int grid, const CUtensorMap& q, const CUtensorMap& k,
+                          const CUtensorMap& v, const CUtensorMap& kp, const CUtensorMap& vp,
+                          cudaStream_t s) {
+  const auto kern = paged_attn_kernel<DP, E>;
+  constexpr int smem = smem_bytes<DP, true>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(kern, dim3(grid), dim3(kBlock), smem, s, q, k, v, kp, vp, a);
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  return launch_after(paged_merge_kernel<DP, E>, dim3(grid, (a.part_rows + 7) / 8), dim3(256), 0, s,
+                      a);
+}
+
+}  // namespace attn
+
+size_t paged_attn_workspace_bytes(const tgdn_tree& t, int H_q, int H_kv, int d) {
+  return attn::split_of(t.n_max, H_q / H_kv, d).bytes;
+}
+
+cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q, int H_kv, int d,
+                              int io, float scale, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const CUtensorMap& kp, const CUtensorMap& vp,
+                              const void* v_rows, int64_t v_stride, void* o, int64_t o_stride,
+                              void* ws, size_t ws_bytes, cudaStream_t s) {
+  using namespace attn;
+  Args a{};
+  a.B = t.B;
+  a.T = t.T;
+  a.H_q = H_q;
+  a.H_kv = H_kv;
+  a.G = H_q / H_kv;
+  a.d = d;
+  a.tpt = kRows / a.G;
+  a.gbox = 128 * a.G * a.tpt;
+  a.tiles = 2;
+  a.scale = scale;
+  a.cu = t.cu_nodes;
+  a.status = t.status;
+  a.o = o;
+  a.o_stride = o_stride;
+  a.v = v_rows;
+  a.v_stride = v_stride;
+  a.n_max = t.n_max;
+  a.words = t.words;
+  a.ps = pg.page_size;
+  a.n_pages = pg.n_pages;
+  a.max_pages = pg.max_pages;
+  a.order = t.order;
+  a.pos = t.pos;
+  a.anc = t.anc;
+  a.table = pg.table;
+  a.len = pg.len;
+  a.held = pg.held;
+  const Split p = split_of(t.n_max, a.G, d);
+  a.part_rows = p.rows;
+  if (ws != nullptr && ws_bytes >= p.bytes) {
+    a.desc = static_cast<int4*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
+  }
+  if (d > 64)
+    return io == TGDN_BF16 ? launch<128, __nv_bfloat16>(a, p.grid, q, k, v, kp, vp, s)
+                           : launch<128, __half>(a, p.grid, q, k, v, kp, vp, s);
+  return io == TGDN_BF16 ? launch<64, __nv_bfloat16>(a, p.grid, q, k, v, kp, vp, s)
+                         : launch<64, __half>(a, p.grid, q, k, v, kp, vp, s);
+}
+
+}  // namespace tgdn

@@ -1,0 +1,134 @@
+// prompt_attn.cu — causal attention over whole prompts (packed rows, grouped heads).
+//
+//   o_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   within each sequence.
+//
+// The pipeline of attn_core.cuh over items (sequence, block of 2 x 128 query rows,
+// key/value head).  The kernel is persistent, one CTA per SM; items go out with each
+// sequence's last (longest) blocks first, the turns alternating in direction, so that the
+// CTAs' shares of the triangle even out without any count kept in memory.
+#include "attn_core.cuh"
+
+namespace tgdn {
+namespace attn {
+
+struct PromptWork {
+  const Args& a;
+  int lane, chunk = 0;       // sequences from `chunk` on ...
+  int before = 0;            // ... begin at this item
+  int turn = 0;
+
+  __device__ explicit PromptWork(const Args& args) : a(args), lane(threadIdx.x & 31) {}
+
+  static __device__ __forceinline__ bool valid(const Args& a, int lo, int hi) {
+    return lo >= 0 && hi >= lo && hi <= a.T;
+  }
+  static __device__ void first(const Args& a, int ft) {
+    if (blockIdx.x != 0) return;
+    for (int b = ft; b < a.B; b += 64)
+      a.status[b] = valid(a, a.cu[b], a.cu[b + 1]) ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
+  }
+  __device__ bool next(Seg& s) {
+    const int grid = gridDim.x, c = blockIdx.x;
+    const int64_t x = (int64_t)turn * grid + ((turn & 1) ? grid - 1 - c : c);
+    ++turn;
+    const int blk = a.tpt * a.tiles;  // tokens per item
+    for (; chunk < a.B; chunk += 32) {
+      int lo = 0, N = 0;
+      if (chunk + lane < a.B) {
+        lo = a.cu[chunk + lane];
+        const int hi = a.cu[chunk + lane + 1];
+        N = valid(a, lo, hi) ? hi - lo : 0;
+      }
+      const int items = (N + blk - 1) / blk * a.H_kv;
+      int upto = items;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, upto, 31);
+      if (x < (int64_t)before + total) {
+        const int at = (int)(x - before);
+        const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+        s.b = chunk + f;
+        s.lo = __shfl_sync(0xffffffffu, lo, f);
+        s.N = __shfl_sync(0xffffffffu, N, f);
+        const int in = at - __shfl_sync(0xffffffffu, upto - items, f);
+        const int blocks = (s.N + blk - 1) / blk;
+        s.hk = in % a.H_kv;
+        s.tok0 = (blocks - 1 - in / a.H_kv) * blk;
+        s.u0 = 0;
+        s.e0 = (min(s.tok0 + a.tpt, s.N) - 1) / kKeys + 1;
+        s.e1 = a.tiles > 1 && s.tok0 + a.tpt < s.N
+                   ? (min(s.tok0 + 2 * a.tpt, s.N) - 1) / kKeys + 1 : 0;
+        s.u1 = max(s.e0, s.e1);
+        s.P = s.npre = 0;
+        s.part = -1;
+        s.zero = 0;
+        return true;
+      }
+      before += total;
+    }
+    return false;
+  }
+};
+
+template <int DP, typename E>
+__global__ void __launch_bounds__(kBlock, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
+                   const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
+  extern __shared__ uint8_t pa_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(pa_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  pipeline<DP, E, false, PromptWork>(smem, a, &qmap, &kmap, &vmap, nullptr, nullptr);
+}
+
+template <int DP, typename E>
+static cudaError_t launch(const Args& a, const CUtensorMap& q, const CUtensorMap& k,
+                          const CUtensorMap& v, int grid, cudaStream_t s) {
+  const auto kern = prompt_attn_kernel<DP, E>;
+  constexpr int smem = smem_bytes<DP, false>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_after(kern, dim3(grid), dim3(kBlock), smem, s, q, k, v, a);
+}
+
+}  // namespace attn
+
+cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, float scale,
+                               const int32_t* cu, const CUtensorMap& q, const CUtensorMap& k,
+                               const CUtensorMap& v, const void* v_rows, int64_t v_stride,
+                               void* o, int64_t o_stride, int32_t* status, cudaStream_t s) {
+  using namespace attn;
+  Args a{};
+  a.B = B;
+  a.T = T;
+  a.H_q = H_q;
+  a.H_kv = H_kv;
+  a.G = H_q / H_kv;
+  a.d = d;
+  a.tpt = kRows / a.G;
+  a.gbox = 128 * a.G * a.tpt;
+  a.scale = scale;
+  a.cu = cu;
+  a.status = status;
+  a.o = o;
+  a.o_stride = o_stride;
+  a.v = v_rows;
+  a.v_stride = v_stride;
+  // at most T / blk + B blocks per head; one row tile per item when two would leave SMs idle
+  const int sms = device_sm_count();
+  auto items = [&](int tiles) { return ((long)T / (a.tpt * tiles) + B) * H_kv; };
+  a.tiles = items(2) >= sms ? 2 : 1;
+  const long n = items(a.tiles);
+  if (n > 0x3fffffffL) return cudaErrorInvalidConfiguration;
+  const int grid = (int)(n < sms ? n : sms);
+  if (d > 64)
+    return io == TGDN_BF16 ? launch<128, __nv_bfloat16>(a, q, k, v, grid, s)
+                           : launch<128, __half>(a, q, k, v, grid, s);
+  return io == TGDN_BF16 ? launch<64, __nv_bfloat16>(a, q, k, v, grid, s)
+                         : launch<64, __half>(a, q, k, v, grid, s);
+}
+
+}  // namespace tgdn

@@ -398,6 +398,297 @@ int tgdn_commit(const tgdn_tree* tree, const tgdn_dims* dims, const int32_t* acc
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// The verifier's attention layers: rotary positions, prompt attention, the paged cache.
+// ---------------------------------------------------------------------------
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
+
+// Rows [rows][heads][d] with `stride` elements between rows: heads contiguous, every row and
+// head on a 16-byte boundary.
+bool rows_ok(const void* p, int64_t stride, int heads, int d) {
+  return aligned16(p) && stride % 8 == 0 && stride >= (int64_t)heads * d && stride < (1ll << 38);
+}
+
+// A tensor of 2-byte elements [n2][n1][d] (element strides s2, s1) as a 3-D map with box
+// {64, box1, box2} and 128-byte swizzle; columns past d read as zeros.
+bool encode_map(CUtensorMap* map, int io, const void* base, int d, int64_t n1, int64_t n2,
+                int64_t s1, int64_t s2, int box1, int box2) {
+  auto fn = encode_fn();
+  if (!fn || n1 < 1 || n2 < 1) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, io == TGDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int check_attn(int32_t H_q, int32_t H_kv, int32_t d, int32_t io, float scale) {
+  if (H_q < 1 || H_kv < 1 || H_q % H_kv != 0 || d < 1) return TGDN_EINVAL;
+  if (!(scale > 0.f && isfinite(scale))) return TGDN_EINVAL;
+  if (d > TGDN_MAX_HEAD_DIM) return TGDN_ETOOBIG;
+  if (d % 8 != 0 || H_q / H_kv > 128 || (io != TGDN_BF16 && io != TGDN_F16))
+    return TGDN_EUNSUPPORTED;
+  return TGDN_OK;
+}
+
+int check_pages(const tgdn_pages* p) {
+  if (!p || p->B < 0 || p->n_pages < 0 || p->max_pages < 0) return TGDN_EINVAL;
+  if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) != 0)
+    return TGDN_EINVAL;
+  if (p->n_pages > (1 << 28) || p->max_pages > (1 << 24) || p->B > (1 << 24)) return TGDN_ETOOBIG;
+  if (p->B > 0 && (!p->len || !p->held || !p->status || (p->max_pages > 0 && !p->table)))
+    return TGDN_EINVAL;
+  if (p->n_pages > 0 && !p->refs) return TGDN_EINVAL;
+  return TGDN_OK;
+}
+
+int check_pool(const tgdn_pages& p, const tgdn_pool* pool) {
+  if (!pool || pool->layers < 1 || pool->H_kv < 1 || pool->d < 8 || pool->d % 8 != 0)
+    return TGDN_EINVAL;
+  if (pool->d > 256 || (int64_t)pool->layers * 2 * pool->H_kv > 65534) return TGDN_ETOOBIG;
+  if ((p.n_pages > 0 && !pool->data) || !aligned16(pool->data)) return TGDN_EINVAL;
+  return TGDN_OK;
+}
+
+bool ws256(const void* ws) { return ws && reinterpret_cast<uintptr_t>(ws) % 256 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int tgdn_rope_freqs(int32_t rot, double theta, int32_t scaling, double factor,
+                    int32_t orig_len, double beta_fast, double beta_slow, uint64_t* freq,
+                    float* mscale) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  if (rot < 2 || rot % 2 != 0 || !freq || !mscale) return TGDN_EINVAL;
+  if (rot > TGDN_ROPE_MAX_DIM) return TGDN_ETOOBIG;
+  if (!(theta > 1.0 && std::isfinite(theta))) return TGDN_EINVAL;
+  if (scaling < TGDN_ROPE_NONE || scaling > TGDN_ROPE_YARN) return TGDN_EINVAL;
+  if (scaling != TGDN_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor))) return TGDN_EINVAL;
+  if (scaling == TGDN_ROPE_NTK && rot < 4) return TGDN_EINVAL;
+  if (scaling == TGDN_ROPE_YARN &&
+      (orig_len < 1 || !(beta_slow > 0.0 && beta_fast > beta_slow && std::isfinite(beta_fast))))
+    return TGDN_EINVAL;
+  if (scaling == TGDN_ROPE_NTK) theta *= std::pow(factor, (double)rot / (rot - 2));
+  // the pair that turns `turns` times within orig_len positions
+  auto pair_of = [&](double turns) {
+    return rot * std::log(orig_len / (turns * kTwoPi)) / (2.0 * std::log(theta));
+  };
+  double lo = 0.0, hi = 1.0;
+  if (scaling == TGDN_ROPE_YARN) {
+    lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+    hi = std::fmin(std::ceil(pair_of(beta_slow)), rot - 1.0);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(theta, -2.0 * i / rot);
+    if (scaling == TGDN_ROPE_LINEAR) {
+      f /= factor;
+    } else if (scaling == TGDN_ROPE_YARN) {
+      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      f = f / factor * r + f * (1.0 - r);
+    }
+    freq[i] = static_cast<uint64_t>(std::ldexp(f / kTwoPi, 64));
+  }
+  *mscale = scaling == TGDN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return TGDN_OK;
+}
+
+int tgdn_rope(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d, int32_t rot,
+              int32_t interleaved, int32_t transpose, int32_t io, float mscale,
+              const uint64_t* freq, const int32_t* cu, const int32_t* base,
+              const int32_t* off, const void* q, int64_t q_stride, const void* k,
+              int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+              int64_t k_out_stride, tgdn_stream_t stream) {
+  CallRange range_("tgdn_rope");
+  if (B < 0 || T < 0 || H_q < 1 || H_kv < 0 || d < 8 || d % 8 != 0 || rot < 2 || rot % 2 != 0 ||
+      rot > d)
+    return TGDN_EINVAL;
+  if (d > 256 || H_q > 1024 || H_kv > 1024) return TGDN_ETOOBIG;
+  if (io != TGDN_F32 && io != TGDN_BF16 && io != TGDN_F16) return TGDN_EINVAL;
+  if (!isfinite(mscale)) return TGDN_EINVAL;
+  if (B == 0 || T == 0) return TGDN_OK;
+  if (!freq || !cu || !q || !q_out || (H_kv > 0 && (!k || !k_out))) return TGDN_EINVAL;
+  if (!rows_ok(q, q_stride, H_q, d) || !rows_ok(q_out, q_out_stride, H_q, d)) return TGDN_EINVAL;
+  if (H_kv > 0 && (!rows_ok(k, k_stride, H_kv, d) || !rows_ok(k_out, k_out_stride, H_kv, d)))
+    return TGDN_EINVAL;
+  // in place means the very rows: a shifted or differently strided overlap would be read
+  // after it was written
+  if ((q == q_out && q_stride != q_out_stride) || (H_kv > 0 && k == k_out && k_stride != k_out_stride))
+    return TGDN_EINVAL;
+  const tgdn::RopeArgs a{B,    T,   H_q, H_kv, d, rot, interleaved != 0, transpose != 0, mscale,
+                         freq, cu,  base, off,  q, k,  q_out, k_out,
+                         q_stride, k_stride, q_out_stride, k_out_stride};
+  return from_cuda(tgdn::launch_rope(a, io, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tgdn_prompt_attention_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t) {
+  return 0;  // items are never split
+}
+
+int tgdn_prompt_attention(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d,
+                          int32_t io, const int32_t* cu, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          float scale, void* o, int64_t o_stride, int32_t* status, void*,
+                          size_t, tgdn_stream_t stream) {
+  CallRange range_("tgdn_prompt_attention");
+  if (B < 0 || T < 0) return TGDN_EINVAL;
+  const int rc = check_attn(H_q, H_kv, d, io, scale);
+  if (rc != TGDN_OK) return rc;
+  if (B == 0) return TGDN_OK;
+  if (!cu || !status) return TGDN_EINVAL;
+  if (T > 0) {
+    if (!q || !k || !v || !o) return TGDN_EINVAL;
+    if (!rows_ok(q, q_stride, H_q, d) || !rows_ok(k, k_stride, H_kv, d) ||
+        !rows_ok(v, v_stride, H_kv, d) || !rows_ok(o, o_stride, H_q, d))
+      return TGDN_EINVAL;
+  }
+  const int G = H_q / H_kv;
+  CUtensorMap qm{}, km{}, vm{};
+  if (T > 0 && (!encode_map(&qm, io, q, d, H_q, T, d, q_stride, G, 128 / G) ||
+                !encode_map(&km, io, k, d, H_kv, T, d, k_stride, 1, 128) ||
+                !encode_map(&vm, io, v, d, H_kv, T, d, v_stride, 1, 128)))
+    return TGDN_ECUDA;
+  return from_cuda(tgdn::launch_prompt_attn(B, T, H_q, H_kv, d, io, scale, cu, qm, km, vm, v,
+                                            v_stride, o, o_stride, status,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tgdn_pages_workspace_bytes(const tgdn_pages* pages) {
+  return check_pages(pages) == TGDN_OK ? tgdn::pages_workspace_bytes(*pages) : 0;
+}
+
+int tgdn_pages_reserve(const tgdn_pages* pages, const int32_t* add, void* ws,
+                       tgdn_stream_t stream) {
+  CallRange range_("tgdn_pages_reserve");
+  const int rc = check_pages(pages);
+  if (rc != TGDN_OK) return rc;
+  if (pages->B == 0) return TGDN_OK;
+  if (!add || !ws256(ws)) return TGDN_EINVAL;
+  return from_cuda(tgdn::launch_pages_reserve(*pages, add, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int tgdn_pages_append(const tgdn_pages* pages, const tgdn_pool* pool, int32_t T,
+                      const int32_t* cu, const int32_t* path, int32_t path_len,
+                      const int32_t* n_path, const void* k, int64_t k_layer, int64_t k_row,
+                      const void* v, int64_t v_layer, int64_t v_row, int32_t advance,
+                      tgdn_stream_t stream) {
+  CallRange range_("tgdn_pages_append");
+  int rc = check_pages(pages);
+  if (rc != TGDN_OK) return rc;
+  rc = check_pool(*pages, pool);
+  if (rc != TGDN_OK) return rc;
+  if (T < 0 || path_len < 0 || (path && !n_path)) return TGDN_EINVAL;
+  if (pages->B == 0) return TGDN_OK;
+  if (!cu) return TGDN_EINVAL;
+  if (T > 0) {
+    if (!k || !v || !rows_ok(k, k_row, pool->H_kv, pool->d) || !rows_ok(v, v_row, pool->H_kv, pool->d))
+      return TGDN_EINVAL;
+    if (pool->layers > 1 && (k_layer % 8 != 0 || v_layer % 8 != 0 || k_layer < 0 || v_layer < 0))
+      return TGDN_EINVAL;
+  }
+  const tgdn::AppendArgs a{*pages, *pool, T, path_len, cu, path, n_path, k, v,
+                           k_layer, k_row, v_layer, v_row};
+  return from_cuda(tgdn::launch_pages_append(a, advance != 0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int tgdn_pages_fork(const tgdn_pages* pages, const tgdn_pool* pool, int32_t n,
+                    const int32_t* src, const int32_t* dst, int32_t* status, void* ws,
+                    tgdn_stream_t stream) {
+  CallRange range_("tgdn_pages_fork");
+  int rc = check_pages(pages);
+  if (rc != TGDN_OK) return rc;
+  rc = check_pool(*pages, pool);
+  if (rc != TGDN_OK) return rc;
+  if (n < 0) return TGDN_EINVAL;
+  if (n > TGDN_PAGES_MAX_LIST) return TGDN_ETOOBIG;
+  if (n == 0) return TGDN_OK;
+  if (!src || !dst || !status || !ws256(ws)) return TGDN_EINVAL;
+  return from_cuda(tgdn::launch_pages_fork(*pages, *pool, n, src, dst, status, ws,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int tgdn_pages_free(const tgdn_pages* pages, int32_t n, const int32_t* seq, tgdn_stream_t stream) {
+  CallRange range_("tgdn_pages_free");
+  const int rc = check_pages(pages);
+  if (rc != TGDN_OK) return rc;
+  if (n < 0 || (n > 0 && !seq)) return TGDN_EINVAL;
+  if (n == 0 || pages->B == 0) return TGDN_OK;
+  return from_cuda(tgdn::launch_pages_free(*pages, n, seq, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int tgdn_pages_compact(const tgdn_pages* pages, const tgdn_pool* pool, int32_t* n_live, void* ws,
+                       tgdn_stream_t stream) {
+  CallRange range_("tgdn_pages_compact");
+  int rc = check_pages(pages);
+  if (rc != TGDN_OK) return rc;
+  rc = check_pool(*pages, pool);
+  if (rc != TGDN_OK) return rc;
+  if (!n_live || !ws256(ws)) return TGDN_EINVAL;
+  return from_cuda(tgdn::launch_pages_compact(*pages, *pool, n_live, ws,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tgdn_paged_tree_attention_workspace_bytes(const tgdn_tree* tree, int32_t H_q, int32_t H_kv,
+                                                 int32_t d) {
+  if (check_tree(tree) != TGDN_OK || check_attn(H_q, H_kv, d, TGDN_BF16, 1.f) != TGDN_OK) return 0;
+  return tgdn::paged_attn_workspace_bytes(*tree, H_q, H_kv, d);
+}
+
+int tgdn_paged_tree_attention(const tgdn_tree* tree, const tgdn_pages* pages, int32_t H_q,
+                              int32_t H_kv, int32_t d, int32_t io, const void* q,
+                              int64_t q_stride, const void* k_tree, int64_t k_stride,
+                              const void* v_tree, int64_t v_stride, const void* k_pages,
+                              const void* v_pages, float scale, void* o, int64_t o_stride,
+                              void* ws, size_t ws_bytes, tgdn_stream_t stream) {
+  CallRange range_("tgdn_paged_tree_attention");
+  int rc = check_tree(tree);
+  if (rc != TGDN_OK) return rc;
+  rc = check_pages(pages);
+  if (rc != TGDN_OK) return rc;
+  rc = check_attn(H_q, H_kv, d, io, scale);
+  if (rc != TGDN_OK) return rc;
+  const tgdn_tree& t = *tree;
+  const tgdn_pages& p = *pages;
+  if (p.B != t.B) return TGDN_EINVAL;
+  if ((int64_t)p.n_pages * H_kv > 0x7fffffff) return TGDN_ETOOBIG;
+  if (p.n_pages > 0 && (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages)))
+    return TGDN_EINVAL;
+  if (ws && !ws256(ws)) return TGDN_EINVAL;
+  if (t.T > 0) {
+    if (!q || !k_tree || !v_tree || !o) return TGDN_EINVAL;
+    if (!rows_ok(q, q_stride, H_q, d) || !rows_ok(k_tree, k_stride, H_kv, d) ||
+        !rows_ok(v_tree, v_stride, H_kv, d) || !rows_ok(o, o_stride, H_q, d))
+      return TGDN_EINVAL;
+  }
+  if (t.B == 0 || t.T == 0) return TGDN_OK;
+  const int G = H_q / H_kv, ps = p.page_size;
+  CUtensorMap qm, km, vm, kp, vp;
+  if (!encode_map(&qm, io, q, d, H_q, t.T, d, q_stride, G, 128 / G) ||
+      !encode_map(&km, io, k_tree, d, H_kv, t.T, d, k_stride, 1, 128) ||
+      !encode_map(&vm, io, v_tree, d, H_kv, t.T, d, v_stride, 1, 128))
+    return TGDN_ECUDA;
+  if (p.n_pages > 0) {
+    const int64_t slabs = (int64_t)p.n_pages * H_kv;
+    const int box = ps < 128 ? ps : 128;
+    if (!encode_map(&kp, io, k_pages, d, ps, slabs, d, (int64_t)ps * d, box, 1) ||
+        !encode_map(&vp, io, v_pages, d, ps, slabs, d, (int64_t)ps * d, box, 1))
+      return TGDN_ECUDA;
+  } else {  // no page is ever read
+    kp = km;
+    vp = vm;
+  }
+  return from_cuda(tgdn::launch_paged_attn(t, p, H_q, H_kv, d, io, scale, qm, km, vm, kp, vp, v_tree,
+                                           v_stride, o, o_stride, ws, ws ? ws_bytes : 0,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // tgdn_verify_noalloc: the same verification with the factors kept in a
 // library-owned device array, for callers that cannot allocate.
 // ---------------------------------------------------------------------------

@@ -122,6 +122,53 @@ cudaError_t launch_tree_attn(const tgdn_tree& t, int H_q, int H_kv, int P_max, f
                              const CUtensorMap& vcmap, const int32_t* prefix_len, void* o,
                              void* ws, size_t ws_bytes, cudaStream_t s);
 
+// Rotary positions (elementwise over rows).
+struct RopeArgs {
+  int B, T, H_q, H_kv, d, rot, interleaved, transpose;
+  float mscale;
+  const uint64_t* freq;
+  const int32_t *cu, *base, *off;
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+};
+cudaError_t launch_rope(const RopeArgs& a, int io, cudaStream_t s);
+
+// Causal attention over packed prompts.  Tensor maps, 128-byte swizzled: q [T][H_q][d] with
+// box {64, G, 128 / G}, k and v [T][H_kv][d] with box {64, 1, 128}.
+cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, float scale,
+                               const int32_t* cu, const CUtensorMap& q, const CUtensorMap& k,
+                               const CUtensorMap& v, const void* v_rows, int64_t v_stride,
+                               void* o, int64_t o_stride, int32_t* status, cudaStream_t s);
+
+// Tree attention over a paged cache; kp, vp: pages as [n_pages * H_kv][page_size][d] with
+// box {64, min(page_size, 128), 1}, the other maps as above.
+size_t paged_attn_workspace_bytes(const tgdn_tree& t, int H_q, int H_kv, int d);
+cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q, int H_kv, int d,
+                              int io, float scale, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const CUtensorMap& kp, const CUtensorMap& vp,
+                              const void* v_rows, int64_t v_stride, void* o, int64_t o_stride,
+                              void* ws, size_t ws_bytes, cudaStream_t s);
+
+// The paged cache's bookkeeping and copies.
+size_t pages_workspace_bytes(const tgdn_pages& p);
+cudaError_t launch_pages_reserve(const tgdn_pages& p, const int32_t* add, void* ws, cudaStream_t s);
+struct AppendArgs {
+  tgdn_pages p;
+  tgdn_pool pool;
+  int T, path_len;
+  const int32_t *cu, *path, *n_path;
+  const void *k, *v;
+  int64_t k_layer, k_row, v_layer, v_row;
+};
+cudaError_t launch_pages_append(const AppendArgs& a, bool advance, cudaStream_t s);
+cudaError_t launch_pages_fork(const tgdn_pages& p, const tgdn_pool& pool, int n,
+                              const int32_t* src, const int32_t* dst, int32_t* status, void* ws,
+                              cudaStream_t s);
+cudaError_t launch_pages_free(const tgdn_pages& p, int n, const int32_t* seq, cudaStream_t s);
+cudaError_t launch_pages_compact(const tgdn_pages& p, const tgdn_pool& pool, int32_t* n_live,
+                                 void* ws, cudaStream_t s);
+
 cudaError_t launch_commit(const tgdn_tree& t, const tgdn_dims& d, const int32_t* accept_node,
                           const void* k, const float* U, const float* G, const float* S_in,
                           float* S_out, cudaStream_t s);

@@ -25,7 +25,9 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "tgdn.h")
 
 OK, EINVAL, ETOOBIG, ECUDA, EUNSUPPORTED = 0, -1, -3, -4, -5
 SEQ_OK, SEQ_TOO_BIG, SEQ_BAD_PARENT, SEQ_ROOTS, SEQ_CYCLE, SEQ_TOO_DEEP, SEQ_TIMEOUT = range(7)
-F32, BF16 = 0, 1
+SEQ_BAD_RANGE, SEQ_BAD_PAGE, SEQ_NO_PAGES = 7, 8, 9
+F32, BF16, F16 = 0, 1, 2
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 MAX_NODES, MAX_DEPTH, MAX_HEAD_DIM = 256, 64, 128
 NOALLOC_SCRATCH_BYTES = 20 * 1024 * 1024
 
@@ -47,6 +49,18 @@ class CTree(ctypes.Structure):
 class CDims(ctypes.Structure):
     _fields_ = [("H_qk", ctypes.c_int32), ("H_v", ctypes.c_int32), ("d_k", ctypes.c_int32),
                 ("d_v", ctypes.c_int32), ("io", ctypes.c_int32)]
+
+
+class CPages(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("held", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class CPool(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("data", ctypes.c_void_p)]
 
 
 _lib = None
@@ -85,6 +99,30 @@ def lib() -> ctypes.CDLL:
         L.tgdn_tree_attention_workspace_bytes.restype = ctypes.c_size_t
         L.tgdn_debug_set_wait_hooks.argtypes = [ctypes.c_uint64, ctypes.c_int32]
         L.tgdn_debug_set_wait_hooks.restype = ctypes.c_int
+        i64, f32, f64, size = ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+        L.tgdn_rope_freqs.argtypes = [i32, f64, i32, f64, i32, f64, f64, vp, vp]
+        L.tgdn_rope.argtypes = [i32] * 9 + [f32, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64,
+                                            st]
+        L.tgdn_prompt_attention.argtypes = [i32] * 6 + [vp, vp, i64, vp, i64, vp, i64, f32, vp, i64,
+                                                        vp, vp, size, st]
+        L.tgdn_prompt_attention_workspace_bytes.argtypes = [i32] * 5
+        L.tgdn_prompt_attention_workspace_bytes.restype = size
+        L.tgdn_pages_workspace_bytes.argtypes = [P(CPages)]
+        L.tgdn_pages_workspace_bytes.restype = size
+        L.tgdn_pages_reserve.argtypes = [P(CPages), vp, vp, st]
+        L.tgdn_pages_append.argtypes = [P(CPages), P(CPool), i32, vp, vp, i32, vp, vp, i64, i64, vp,
+                                        i64, i64, i32, st]
+        L.tgdn_pages_fork.argtypes = [P(CPages), P(CPool), i32, vp, vp, vp, vp, st]
+        L.tgdn_pages_free.argtypes = [P(CPages), i32, vp, st]
+        L.tgdn_pages_compact.argtypes = [P(CPages), P(CPool), vp, vp, st]
+        L.tgdn_paged_tree_attention.argtypes = [P(CTree), P(CPages), i32, i32, i32, i32, vp, i64, vp,
+                                                i64, vp, i64, vp, vp, f32, vp, i64, vp, size, st]
+        L.tgdn_paged_tree_attention_workspace_bytes.argtypes = [P(CTree), i32, i32, i32]
+        L.tgdn_paged_tree_attention_workspace_bytes.restype = size
+        for f in (L.tgdn_rope_freqs, L.tgdn_rope, L.tgdn_prompt_attention, L.tgdn_pages_reserve,
+                  L.tgdn_pages_append, L.tgdn_pages_fork, L.tgdn_pages_free, L.tgdn_pages_compact,
+                  L.tgdn_paged_tree_attention):
+            f.restype = ctypes.c_int
         L.tgdn_status_string.argtypes = [i32]
         L.tgdn_status_string.restype = ctypes.c_char_p
         L.tgdn_version.argtypes = []
@@ -352,6 +390,239 @@ def verify_noalloc(tree: Tree, dims: Dims, q, k, v, g, b, S0, o, stream=None) ->
             _dev(o, io, T * dims.H_v * dims.d_v, "o"))
     _check(lib().tgdn_verify_noalloc(ctypes.byref(ct), ctypes.byref(cd), *args, _stream(stream)),
            "tgdn_verify_noalloc")
+
+
+# ---------------------------------------------------------------- attention layers
+_IO = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _rows(t: torch.Tensor, dtype, T: int, heads: int, d: int, name: str):
+    """(pointer, elements between rows) of a CUDA tensor [T][heads][d] whose rows may be views
+    of longer ones (heads and elements contiguous)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (the library takes device pointers)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != (T, heads, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, heads, d)}")
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), s[0] if T > 1 else heads * d
+
+
+def _io(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype not in _IO or t.dim() != 3:
+        raise TypeError(f"{name}: expected a float32, bfloat16 or float16 tensor [T][heads][d]")
+    return _IO[t.dtype]
+
+
+def rope_freqs(rot: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               orig_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """tgdn_rope_freqs: (freq, mscale) for rope().  freq [rot / 2] on `device`: each pair's turns
+    per position as 64-bit fractions (int64 storage); scaling "none", "linear", "ntk" or "yarn"."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling: {scaling!r}, expected one of {sorted(ROPE_SCALING)}")
+    freq = torch.empty(max(rot // 2, 1), dtype=torch.int64)
+    mscale = ctypes.c_float()
+    _check(lib().tgdn_rope_freqs(rot, theta, ROPE_SCALING[scaling], factor, orig_len, beta_fast,
+                                 beta_slow, freq.data_ptr(), ctypes.byref(mscale)),
+           "tgdn_rope_freqs")
+    return freq.to(device), mscale.value
+
+
+def rope(q, k, q_out, k_out, freq, *, cu, base=None, off=None, interleaved: bool = False,
+         mscale: float = 1.0, transpose: bool = False, stream=None) -> None:
+    """tgdn_rope: rotary positions of q [T][H_q][d] and k [T][H_kv][d] (k, k_out may be None)
+    into q_out, k_out (the inputs themselves for in place).  The first 2 * len(freq) elements
+    of each head are rotated.  Row t of sequence b (cu [B + 1] int32) is at position
+    base[b] + off[t] (int32; default: its index within the sequence).  transpose=True is the
+    gradient."""
+    io = _io(q, "q")
+    T, H_q, d = q.shape
+    H_kv = 0 if k is None else k.shape[1]
+    B = cu.numel() - 1
+    qp, qs = _rows(q, q.dtype, T, H_q, d, "q")
+    qop, qos = _rows(q_out, q.dtype, T, H_q, d, "q_out")
+    kp = kop = None
+    ks = kos = 0
+    if k is not None:
+        kp, ks = _rows(k, q.dtype, T, H_kv, d, "k")
+        kop, kos = _rows(k_out, q.dtype, T, H_kv, d, "k_out")
+    i32 = torch.int32
+    _check(lib().tgdn_rope(B, T, H_q, H_kv, d, 2 * freq.numel(), int(interleaved), int(transpose),
+                           io, mscale, _dev(freq, torch.int64, freq.numel(), "freq"),
+                           _dev(cu, i32, B + 1, "cu"),
+                           None if base is None else _dev(base, i32, B, "base"),
+                           None if off is None else _dev(off, i32, T, "off"),
+                           qp, qs, kp, ks, qop, qos, kop, kos, _stream(stream)), "tgdn_rope")
+
+
+def prompt_attention_workspace_bytes(B: int, T: int, H_q: int, H_kv: int, d: int) -> int:
+    return int(lib().tgdn_prompt_attention_workspace_bytes(B, T, H_q, H_kv, d))
+
+
+def prompt_attention(cu, q, k, v, o, scale: float, status, ws=None, stream=None) -> None:
+    """tgdn_prompt_attention: causal attention over whole prompts packed one after another
+    (cu [B + 1] int32).  q, o [T][H_q][d], k, v [T][H_kv][d] (bf16 or f16; rows may be views of
+    a fused projection); status [B] int32 is written."""
+    io = _io(q, "q")
+    T, H_q, d = q.shape
+    H_kv = k.shape[1]
+    B = cu.numel() - 1
+    qp, qs = _rows(q, q.dtype, T, H_q, d, "q")
+    kp, ks = _rows(k, q.dtype, T, H_kv, d, "k")
+    vp, vs = _rows(v, q.dtype, T, H_kv, d, "v")
+    op, os_ = _rows(o, q.dtype, T, H_q, d, "o")
+    wsp, wsn = _workspace(ws)
+    _check(lib().tgdn_prompt_attention(B, T, H_q, H_kv, d, io, _dev(cu, torch.int32, B + 1, "cu"),
+                                       qp, qs, kp, ks, vp, vs, scale, op, os_,
+                                       _dev(status, torch.int32, B, "status"), wsp, wsn,
+                                       _stream(stream)), "tgdn_prompt_attention")
+
+
+def _workspace(ws):
+    if ws is None or ws.numel() == 0:
+        return None, 0
+    return _dev(ws, ws.dtype, ws.numel(), "ws"), ws.numel() * ws.element_size()
+
+
+class Pages:
+    """A paged key/value cache's bookkeeping on the device (empty at first), shared by the
+    layers: table [B][max_pages], len, held, status [B], refs [n_pages] (int32)."""
+
+    def __init__(self, B: int, n_pages: int, page_size: int, max_pages: int, device="cuda"):
+        self.B, self.n_pages = int(B), int(n_pages)
+        self.page_size, self.max_pages = int(page_size), int(max_pages)
+        new = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        self.table = new(self.B, self.max_pages)
+        self.len, self.held, self.status = new(self.B), new(self.B), new(self.B)
+        self.refs = new(self.n_pages)
+
+    def c(self) -> CPages:
+        i32, B = torch.int32, self.B
+        return CPages(B, self.n_pages, self.page_size, self.max_pages,
+                      _dev(self.table, i32, B * self.max_pages, "table"),
+                      _dev(self.len, i32, B, "len"), _dev(self.held, i32, B, "held"),
+                      _dev(self.refs, i32, self.n_pages, "refs"),
+                      _dev(self.status, i32, B, "status"))
+
+    def pool(self, layers: int, H_kv: int, d: int, dtype=torch.bfloat16) -> torch.Tensor:
+        """An uninitialised pool [layers][2 (keys, values)][n_pages][H_kv][page_size][d]."""
+        return torch.empty((layers, 2, self.n_pages, H_kv, self.page_size, d), dtype=dtype,
+                           device=self.table.device)
+
+
+def _pool(pages: Pages, pool: torch.Tensor) -> CPool:
+    if not isinstance(pool, torch.Tensor) or pool.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("pool: expected a bfloat16 or float16 tensor")
+    if pool.dim() != 6 or pool.shape[1] != 2 or pool.shape[2] != pages.n_pages or \
+            pool.shape[4] != pages.page_size:
+        raise ValueError(f"pool: shape {tuple(pool.shape)}, expected "
+                         "(layers, 2, n_pages, H_kv, page_size, d)")
+    return CPool(pool.shape[0], pool.shape[3], pool.shape[5],
+                 _dev(pool, pool.dtype, pool.numel(), "pool"))
+
+
+def pages_workspace_bytes(pages: Pages) -> int:
+    return int(lib().tgdn_pages_workspace_bytes(ctypes.byref(pages.c())))
+
+
+def pages_workspace(pages: Pages) -> torch.Tensor:
+    """A workspace for the page calls of this cache."""
+    n = pages_workspace_bytes(pages)
+    if n == 0:
+        raise TgdnError(EINVAL, "tgdn_pages_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=pages.table.device)
+
+
+def _pages_ws(pages: Pages, ws) -> int:
+    return _dev(ws, torch.uint8, pages_workspace_bytes(pages), "ws")
+
+
+def pages_reserve(pages: Pages, add, ws, stream=None) -> None:
+    """tgdn_pages_reserve: pages for add[b] more positions of every sequence (int32 [B])."""
+    _check(lib().tgdn_pages_reserve(ctypes.byref(pages.c()),
+                                    _dev(add, torch.int32, pages.B, "add"), _pages_ws(pages, ws),
+                                    _stream(stream)), "tgdn_pages_reserve")
+
+
+def pages_append(pages: Pages, cu, k, v, pool, path=None, n_path=None, advance: bool = True,
+                 stream=None) -> None:
+    """tgdn_pages_append: keys and values k, v [layers][T][H_kv][d] (or [T][H_kv][d] for a pool of
+    one layer) to positions len[b], ...: the rows cu[b] .. cu[b+1] - 1, or with path
+    [B][path_len] the rows cu[b] + path[b][i], i < n_path[b].  advance=False keeps len."""
+    cp = _pool(pages, pool)
+    ptr = []
+    for t, name in ((k, "k"), (v, "v")):
+        if isinstance(t, torch.Tensor) and t.dim() == 3:
+            t = t.unsqueeze(0)
+        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != cp.layers:
+            raise ValueError(f"{name}: expected a tensor [{cp.layers}][T][H_kv][d]")
+        p, row = _rows(t[0], pool.dtype, k.shape[-3], cp.H_kv, cp.d, name)
+        ptr += [p, t.stride(0) if cp.layers > 1 else 0, row]
+    plen = 0 if path is None else path.shape[1]
+    i32, B = torch.int32, pages.B
+    _check(lib().tgdn_pages_append(ctypes.byref(pages.c()), ctypes.byref(cp), k.shape[-3],
+                                   _dev(cu, i32, B + 1, "cu"),
+                                   None if path is None else _dev(path, i32, B * plen, "path"), plen,
+                                   None if path is None else _dev(n_path, i32, B, "n_path"),
+                                   *ptr, int(advance), _stream(stream)), "tgdn_pages_append")
+
+
+def pages_fork(pages: Pages, src, dst, pool, status, ws, stream=None) -> None:
+    """tgdn_pages_fork: sequence dst[i] becomes a copy of src[i] (int32 [n]); status [n] int32."""
+    n, i32 = src.numel(), torch.int32
+    _check(lib().tgdn_pages_fork(ctypes.byref(pages.c()), ctypes.byref(_pool(pages, pool)), n,
+                                 _dev(src, i32, n, "src"), _dev(dst, i32, n, "dst"),
+                                 _dev(status, i32, n, "status"), _pages_ws(pages, ws),
+                                 _stream(stream)), "tgdn_pages_fork")
+
+
+def pages_free(pages: Pages, seq, stream=None) -> None:
+    """tgdn_pages_free: releases the pages of the listed sequences (int32)."""
+    _check(lib().tgdn_pages_free(ctypes.byref(pages.c()), seq.numel(),
+                                 _dev(seq, torch.int32, seq.numel(), "seq"), _stream(stream)),
+           "tgdn_pages_free")
+
+
+def pages_compact(pages: Pages, pool, n_live, ws, stream=None) -> None:
+    """tgdn_pages_compact: live pages to the front of the pool; n_live [1] int32 is written."""
+    _check(lib().tgdn_pages_compact(ctypes.byref(pages.c()), ctypes.byref(_pool(pages, pool)),
+                                    _dev(n_live, torch.int32, 1, "n_live"), _pages_ws(pages, ws),
+                                    _stream(stream)), "tgdn_pages_compact")
+
+
+def paged_tree_attention_workspace_bytes(tree: Tree, pages: Pages, H_q: int, H_kv: int,
+                                         d: int) -> int:
+    return int(lib().tgdn_paged_tree_attention_workspace_bytes(ctypes.byref(tree.c()), H_q, H_kv, d))
+
+
+def paged_tree_attention(tree: Tree, pages: Pages, q, k_tree, v_tree, k_pages, v_pages, o,
+                         scale: float, ws=None, stream=None) -> None:
+    """tgdn_paged_tree_attention: each node attends to its sequence's cached positions and its
+    own root path.  q/o [T][H_q][d], k_tree/v_tree [T][H_kv][d] (rows may be views of a fused
+    projection), k_pages/v_pages [n_pages][H_kv][page_size][d] (one layer of the pool), bf16 or
+    f16.  ws: optional workspace of paged_tree_attention_workspace_bytes() bytes, with which
+    long contexts are split over CTAs."""
+    io = _io(q, "q")
+    T, H_q, d = q.shape
+    if T != tree.T:
+        raise ValueError(f"q: {T} rows, the tree has {tree.T}")
+    H_kv = k_tree.shape[1]
+    qp, qs = _rows(q, q.dtype, T, H_q, d, "q")
+    kp, ks = _rows(k_tree, q.dtype, T, H_kv, d, "k_tree")
+    vp, vs = _rows(v_tree, q.dtype, T, H_kv, d, "v_tree")
+    op, os_ = _rows(o, q.dtype, T, H_q, d, "o")
+    n = pages.n_pages * H_kv * pages.page_size * d
+    wsp, wsn = _workspace(ws)
+    _check(lib().tgdn_paged_tree_attention(ctypes.byref(tree.c()), ctypes.byref(pages.c()), H_q,
+                                           H_kv, d, io, qp, qs, kp, ks, vp, vs,
+                                           _dev(k_pages, q.dtype, n, "k_pages"),
+                                           _dev(v_pages, q.dtype, n, "v_pages"), scale, op, os_,
+                                           wsp, wsn, _stream(stream)), "tgdn_paged_tree_attention")
 
 
 def debug_set_wait_hooks(wait_limit_ns: int = 0, withhold_item: int = -1) -> None:
