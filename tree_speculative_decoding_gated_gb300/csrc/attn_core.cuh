@@ -134,6 +134,67 @@ __device__ __forceinline__ void ld_wait32(float* r) {
                : "memory");
 }
 
+// Two-wide fp32 arithmetic and the three-input maximum (NaN operands are passed over).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A value that all lanes of the warp hold, so that code depending on it is compiled as
+// warp-uniform (addresses and descriptors in uniform registers).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Tensor-core instructions of a convergent warp, issued by its elected lane (the same lane
+// every time).  Elected in place and with the descriptors' low words apart, an instruction
+// costs its 64 cycles also beside busy warps; under a branch or a predicate computed from the
+// lane number the same instructions took ~92.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024-byte stride, 128B swizzle
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(add), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(add), "r"(kDescHi)
+      : "memory");
+}
+// Arrives on `bar` once every tensor-core instruction of that lane so far is complete.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
 struct Bars {
   uint64_t kvfull[8], kvempty[8];
   uint64_t qfull, qempty, drain;
@@ -204,7 +265,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
   constexpr int NS = L::kStages;
   Bars* br = reinterpret_cast<Bars*>(smem + L::kOffMisc);
   uint8_t* sord = smem + L::kOffMisc + sizeof(Bars);  // [row tile][2][256] order bytes (paged)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = uniform(tid >> 5);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&br->kvfull[i], 1);
@@ -343,105 +405,105 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       if (n_q > 0) (void)mbar_wait(&br->qfull, (n_q - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    // ---------------- products
-    if (lane == 0) {
-      uint32_t cnt = 0, fix = 0;    // tiles seen; value tiles made safe
-      uint32_t done[2] = {0, 0};    // steps of each row tile
-      constexpr uint32_t id_s = idesc(Elem<E>::kFmt, 128, kKeys, 0);
-      constexpr uint32_t id_o = idesc(Elem<E>::kFmt, 128, DP, 1);
-      const uint32_t sQ = smem_addr(smem), sKV = smem_addr(smem + L::kOffKV);
-      auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
-        // the previous O_t += P_t V has read P_t, which lies in S_t's columns
-        if (done[t] > 0 && !mbar_wait_suspend(&br->pvdone[t], (done[t] - 1) & 1, abort)) return false;
-        tc_fence_after_sync();
-        const uint32_t q = sQ + t * L::kTile, k = sKV + (c % NS) * L::kTile;
+    // ---------------- products.  The whole warp runs this role with equal values.
+    uint32_t cnt = 0, fix = 0;    // tiles seen; value tiles made safe
+    uint32_t done[2] = {0, 0};    // steps of each row tile
+    constexpr uint32_t id_s = idesc(Elem<E>::kFmt, 128, kKeys, 0);
+    constexpr uint32_t id_o = idesc(Elem<E>::kFmt, 128, DP, 1);
+    const uint32_t utm = uniform(tmem);
+    // descriptors' low words: address and leading byte offset in 16-byte units (value tiles:
+    // the distance of their two 64-column halves)
+    const uint32_t dQ = (smem_addr(smem) >> 4) | (1u << 16);
+    const uint32_t dK = (smem_addr(smem + L::kOffKV) >> 4) | (1u << 16);
+    const uint32_t dV = (smem_addr(smem + L::kOffKV) >> 4) | ((uint32_t)(L::kHalf >> 4) << 16);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort)) != 0;
+    };
+    auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
+      // the previous O_t += P_t V has read P_t, which lies in S_t's columns
+      if (done[t] > 0 && !wait(&br->pvdone[t], (done[t] - 1) & 1)) return false;
+      tc_fence_after_sync();
+      const uint32_t slot = c % NS;
+      const uint32_t q = dQ + t * (L::kTile >> 4), k = dK + slot * (L::kTile >> 4);
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i)
-          umma_bf16(tmem + t * 128,
-                    smem_desc(q + (i >> 2) * L::kHalf + (i & 3) * 32, 16, 1024, kSwizzle128B),
-                    smem_desc(k + (i >> 2) * L::kHalf + (i & 3) * 32, 16, 1024, kSwizzle128B), id_s,
-                    i > 0);
-        umma_commit(&br->sfull[t]);
-        return true;
-      };
-      auto pv = [&](int t, uint32_t c, bool first) {  // O_t (+)= P_t V of the tile in slot c
-        tc_fence_after_sync();
-        const uint32_t v = sKV + (c % NS) * L::kTile;
+      for (int i = 0; i < DP / 16; ++i) {
+        const uint32_t at = ((i >> 2) * L::kHalf + (i & 3) * 32) >> 4;
+        mma_ss(utm + t * 128, q + at, k + at, id_s, i > 0);
+      }
+      commit(&br->sfull[t]);
+      return true;
+    };
+    auto pv = [&](int t, uint32_t c, bool first) {  // O_t (+)= P_t V of the tile in slot c
+      tc_fence_after_sync();
+      const uint32_t slot = c % NS;
+      const uint32_t v = dV + slot * (L::kTile >> 4);
+      const uint32_t add = first ? 0u : 1u;
 #pragma unroll
-        for (int i = 0; i < kKeys / 16; ++i)
-          umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + i * 8,
-                           smem_desc(v + i * 2048, L::kHalf, 1024, kSwizzle128B), id_o,
-                           (!first || i > 0) ? 1u : 0u);
-        umma_commit(&br->pvdone[t]);
-      };
-      int n = 0;
-      for (; ok; ++n) {
-        const int r = n % kRing;
-        ok = mbar_wait_suspend(&br->segfull[r], (n / kRing) & 1, abort);
-        if (!ok) break;
-        const Seg s = br->seg[r];
-        if (s.b < 0) break;
-        ok = mbar_wait_suspend(&br->qfull, n & 1, abort) &&
-             mbar_wait_suspend(&br->kvfull[cnt % NS], (cnt / NS) & 1, abort);
-        const bool a0 = s.e0 > s.u0, a1 = s.e1 > s.u0;
-        if (ok && a0) ok = score(0, cnt);
-        if (ok && a1) ok = score(1, cnt);
-        if (ok) {
-          umma_commit(&br->kvempty[cnt % NS]);
-          if (s.u1 - s.u0 == 1) umma_commit(&br->qempty);
+      for (int i = 0; i < kKeys / 16; ++i)
+        mma_ts(utm + 256 + t * 128, utm + t * 128 + i * 8, v + i * 128, id_o,
+               i > 0 ? 1u : add);
+      commit(&br->pvdone[t]);
+    };
+    for (int n = 0; ok; ++n) {
+      const int r = n % kRing;
+      ok = wait(&br->segfull[r], (n / kRing) & 1);
+      if (!ok) break;
+      Seg s = br->seg[r];
+      if (uniform(s.b) < 0) break;
+      s.u0 = uniform(s.u0), s.u1 = uniform(s.u1), s.e0 = uniform(s.e0), s.e1 = uniform(s.e1);
+      s.N = uniform(s.N), s.P = uniform(s.P), s.npre = uniform(s.npre), s.tok0 = uniform(s.tok0);
+      ok = wait(&br->qfull, n & 1) && wait(&br->kvfull[cnt % NS], (cnt / NS) & 1);
+      const bool a0 = s.e0 > s.u0, a1 = s.e1 > s.u0;
+      if (ok && a0) ok = score(0, cnt);
+      if (ok && a1) ok = score(1, cnt);
+      if (ok) {
+        commit(&br->kvempty[cnt % NS]);
+        if (s.u1 - s.u0 == 1) commit(&br->qempty);
+      }
+      for (int u = s.u0; ok && u < s.u1; ++u) {
+        const uint32_t cv = cnt + 1, ck = cnt + 2;  // this value tile, the next key tile
+        const bool x0 = u < s.e0, x1 = u < s.e1;    // steps of the row tiles
+        const bool y0 = u + 1 < s.e0, y1 = u + 1 < s.e1;
+        if (x0) ok = wait(&br->pready[0], done[0] & 1);
+        if (ok) ok = wait(&br->kvfull[cv % NS], (cv / NS) & 1);
+        int lim;
+        bool by_row;
+        if (ok && tile_part<PAGED>(s, u, lim, by_row)) {
+          ok = wait(&br->fixed[fix % kFixRing], (fix / kFixRing) & 1);
+          ++fix;
         }
-        for (int u = s.u0; ok && u < s.u1; ++u) {
-          const uint32_t cv = cnt + 1, ck = cnt + 2;  // this value tile, the next key tile
-          const bool x0 = u < s.e0, x1 = u < s.e1;    // steps of the row tiles
-          const bool y0 = u + 1 < s.e0, y1 = u + 1 < s.e1;
-          bool pv1 = !x1;
-          if (x0) ok = mbar_wait_suspend(&br->pready[0], done[0] & 1, abort);
-          if (ok) ok = mbar_wait_suspend(&br->kvfull[cv % NS], (cv / NS) & 1, abort);
-          int lim;
-          bool by_row;
-          if (ok && tile_part<PAGED>(s, u, lim, by_row)) {
-            ok = mbar_wait_suspend(&br->fixed[fix % kFixRing], (fix / kFixRing) & 1, abort);
-            ++fix;
-          }
-          if (!ok) break;
-          if (x0) {
-            pv(0, cv, u == s.u0);
-            ++done[0];
-          }
-          // the other tile's product first if its P is there already: S_0 has to wait for
-          // the product just issued
-          if (!pv1 && mbar_try(&br->pready[1], done[1] & 1)) {
+        if (!ok) break;
+        if (x0) {
+          pv(0, cv, u == s.u0);
+          ++done[0];
+        }
+        if (y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
+        if (ok && x1) {
+          ok = wait(&br->pready[1], done[1] & 1);
+          if (ok) {
             pv(1, cv, u == s.u0);
             ++done[1];
-            pv1 = true;
           }
-          if (y0) ok = mbar_wait_suspend(&br->kvfull[ck % NS], (ck / NS) & 1, abort) && score(0, ck);
-          if (ok && !pv1) {
-            ok = mbar_wait_suspend(&br->pready[1], done[1] & 1, abort);
-            if (ok) {
-              pv(1, cv, u == s.u0);
-              ++done[1];
-            }
-          }
-          if (!ok) break;
-          umma_commit(&br->kvempty[cv % NS]);
-          if (y1) ok = mbar_wait_suspend(&br->kvfull[ck % NS], (ck / NS) & 1, abort) && score(1, ck);
-          if (ok && u + 1 < s.u1) {
-            umma_commit(&br->kvempty[ck % NS]);
-            if (u + 2 == s.u1) umma_commit(&br->qempty);
-          }
-          cnt += 2;
         }
-        if (!ok) {
-          br->where = s.b;
-          break;
+        if (!ok) break;
+        commit(&br->kvempty[cv % NS]);
+        if (y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
+        if (ok && u + 1 < s.u1) {
+          commit(&br->kvempty[ck % NS]);
+          if (u + 2 == s.u1) commit(&br->qempty);
         }
-        mbar_arrive(&br->segempty[r]);
+        cnt += 2;
       }
-      // every product and every arrival it owes is done before the shared memory goes
-      umma_commit(&br->drain);
-      (void)mbar_wait(&br->drain, 0);
+      if (!ok) {
+        if (lane == 0) br->where = s.b;
+        break;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br->segempty[r]);
     }
+    // every product and every arrival it owes is done before the shared memory goes
+    commit(&br->drain);
+    (void)mbar_wait(&br->drain, 0);
     __syncwarp();
   } else if (warp >= kFixWarp) {
     // ---------------- value rows that must not reach the product
@@ -547,7 +609,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
             }
           }
         }
-        float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float m = -INFINITY;
+        float2 la = make_float2(0.f, 0.f), lb = la;  // the row's sum, in four parts
         for (int u = s.u0; u < e; ++u) {
           ok = mbar_wait_suspend(&br->sfull[t], done & 1, abort);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -580,21 +643,20 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
             for (int c = 0; c < kKeys; ++c)
               if (c > lim) x[c] = -INFINITY;
           }
-          float mx[32];
+          float mx[4];  // four chains of three-input maxima
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            mx[c] = fmaxf(fmaxf(x[c], x[c + 32]), fmaxf(x[c + 64], x[c + 96]));
+          for (int j = 0; j < 4; ++j) {
+            mx[j] = fmaxf(x[j * 32], x[j * 32 + 1]);
 #pragma unroll
-          for (int w = 16; w >= 1; w /= 2)
-#pragma unroll
-            for (int c = 0; c < w; ++c) mx[c] = fmaxf(mx[c], mx[c + w]);
+            for (int c = 2; c < 32; c += 2) mx[j] = max3(mx[j], x[j * 32 + c], x[j * 32 + c + 1]);
+          }
+          mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           const bool need = live && mx[0] > m + gap;  // also the first finite maximum
           if (__any_sync(0xffffffffu, need)) {
             const float alpha =
                 need ? (m == -INFINITY ? 0.f : fast_exp2((m - mx[0]) * c2)) : 1.f;
             if (need) m = mx[0];
-            l0 *= alpha;
-            l1 *= alpha;
+            la.x *= alpha, la.y *= alpha, lb.x *= alpha, lb.y *= alpha;
             if (u > s.u0) {  // (the last product on O_t was done before S_t was issued)
 #pragma unroll 1
               for (int q = 0; q < DP / 16; ++q) {
@@ -608,17 +670,19 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
               }
             }
           }
-          const float mc = m == -INFINITY ? 0.f : m * c2;
+          const float mc = m == -INFINITY ? 0.f : -m * c2;
+          const float2 cc = make_float2(c2, c2), mm = make_float2(mc, mc);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float p0 = fast_exp2(fmaf(x[q * 32 + 2 * c], c2, -mc));
-              const float p1 = fast_exp2(fmaf(x[q * 32 + 2 * c + 1], c2, -mc));
-              l0 += p0;
-              l1 += p1;
-              w[c] = Elem<E>::pack(p0, p1);
+              float2 y = fma2(make_float2(x[q * 32 + 2 * c], x[q * 32 + 2 * c + 1]), cc, mm);
+              y.x = fast_exp2(y.x);
+              y.y = fast_exp2(y.y);
+              if (c & 1) lb = add2(lb, y);
+              else la = add2(la, y);
+              w[c] = Elem<E>::pack(y.x, y.y);
             }
             tmem_st16(tS + q * 16, w);
           }
@@ -637,7 +701,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         tc_fence_after_sync();
         const bool dirty = *reinterpret_cast<volatile int*>(&br->dirty[r]) != 0;
         const bool bad = PAGED && (s.zero || *reinterpret_cast<volatile int*>(&br->bad[r]) != 0);
-        const float l = l0 + l1;
+        const float l = (la.x + la.y) + (lb.x + lb.y);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         E* orow = static_cast<E*>(a.o) + (int64_t)(s.lo + tok) * a.o_stride +
                   (int64_t)(s.hk * a.G + g) * a.d;
