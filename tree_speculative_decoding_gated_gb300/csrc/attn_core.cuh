@@ -50,12 +50,12 @@ constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (128 each), O_0, O_1 (128 each)
 constexpr int kMaxNodes = TGDN_MAX_NODES;
 
 // Shared-memory layout for heads padded to DP = 64 or 128 elements.
-template <int DP>
+template <int DP, bool PAGED>
 struct Lay {
   static constexpr int kHalves = DP / 64;               // 128-byte swizzled halves of a row
   static constexpr int kHalf = kKeys * 128;             // one half of a tile
   static constexpr int kTile = kHalf * kHalves;         // a key, value or query tile
-  static constexpr int kStages = DP == 128 ? 5 : 8;     // key and value tiles in flight
+  static constexpr int kStages = DP == 64 ? 8 : PAGED ? 4 : 5;  // key and value tiles in flight
   static constexpr int kOffKV = 2 * kTile;              // (the two query tiles come first)
   static constexpr int kOffMisc = kOffKV + kStages * kTile;
 };
@@ -79,6 +79,7 @@ struct Args {
   int32_t* status;
   void* o;
   int64_t o_stride;                // elements between tokens
+  int o_wide;                      // every row and head of o on a 32-byte boundary
   const void* v;                   // new rows' values (prompt or tree), for the rare exact path
   int64_t v_stride;
   // paged
@@ -86,14 +87,18 @@ struct Args {
   const int32_t *order, *pos, *table, *len, *held;
   const uint64_t* anc;
   int tiles;                       // row tiles per item: 2, or 1 when items are few
-  float* part;                     // partial results (null: items are never split)
+  // partial results (null: items are never split): [slot][DP / 4][part_rows] float4 of O
+  // unnormalised, [slot][part_rows] of (reference maximum in log2 units, sum)
+  float* part;
+  float2* part_ml;
   int4* desc;                      // [grid][2]: the split item that begins in a CTA's range
   int part_rows;                   // rows per partial slot
 };
 
-// A partial row: O (DP), then the reference maximum in log2 units and the sum.
-template <int DP>
-constexpr int part_stride() { return DP + 4; }
+// (o_wide of Args)
+static int wide_rows(const void* o, int64_t stride, int d) {
+  return reinterpret_cast<uintptr_t>(o) % 32 == 0 && stride % 16 == 0 && d % 16 == 0;
+}
 
 template <typename E> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
@@ -132,6 +137,15 @@ __device__ __forceinline__ void ld_wait32(float* r) {
                  "+r"(u[30]), "+r"(u[31])
                :
                : "memory");
+}
+
+// Bounded wait.  What is not there at once is awaited out of line: the roles' loops compete
+// for the instruction cache.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait_suspend(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try(bar, parity) || wait_slow(bar, parity, abort);
 }
 
 // Two-wide fp32 arithmetic and the three-input maximum (NaN operands are passed over).
@@ -186,6 +200,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(id), "r"(add), "r"(kDescHi)
       : "memory");
 }
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global32(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 // Arrives on `bar` once every tensor-core instruction of that lane so far is complete.
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
@@ -195,11 +215,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
-struct Bars {
+struct alignas(16) Bars {
   uint64_t kvfull[8], kvempty[8];
   uint64_t qfull, qempty, drain;
-  uint64_t sfull[2], pready[2], pvdone[2];
-  uint64_t fixed[kFixRing];
+  uint64_t sfull[2], pready[2][2], pvdone[2];
+  uint64_t partfull[kFixRing], fixed[kFixRing];
+  uint64_t maskfull[2], maskempty[2];
   uint64_t segfull[kRing], segempty[kRing];
   Seg seg[kRing];
   int dirty[kRing], bad[kRing];
@@ -208,9 +229,15 @@ struct Bars {
   int where;  // the sequence in work when a wait expired
 };
 
+// Paged: ancestor-or-self sets of an item's nodes (node-index space), two items' worth, and a
+// byte copy of the topological order for each warp that builds them.
+constexpr int kMaskWords = kMaxNodes / 32;
+constexpr int kMaskBytes = 2 * 2 * kRows * kMaskWords * 4;
+static_assert(sizeof(Bars) % 16 == 0, "the masks behind it are read 16 bytes at a time");
+
 template <int DP, bool PAGED>
 constexpr int smem_bytes() {
-  return Lay<DP>::kOffMisc + (int)sizeof(Bars) + (PAGED ? 4 * kMaxNodes : 0) + 1024;
+  return Lay<DP, PAGED>::kOffMisc + (int)sizeof(Bars) + (PAGED ? kMaskBytes + 2 * kMaxNodes : 0) + 1024;
 }
 static_assert(smem_bytes<128, true>() <= 227 * 1024, "fits one CTA per SM");
 
@@ -261,10 +288,11 @@ template <int DP, typename E, bool PAGED, typename W>
 __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUtensorMap* qmap,
                                          const CUtensorMap* kmap, const CUtensorMap* vmap,
                                          const CUtensorMap* kpmap, const CUtensorMap* vpmap) {
-  using L = Lay<DP>;
+  using L = Lay<DP, PAGED>;
   constexpr int NS = L::kStages;
   Bars* br = reinterpret_cast<Bars*>(smem + L::kOffMisc);
-  uint8_t* sord = smem + L::kOffMisc + sizeof(Bars);  // [row tile][2][256] order bytes (paged)
+  uint32_t* smask = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + sizeof(Bars));  // [2][256][8]
+  uint8_t* sord = smem + L::kOffMisc + sizeof(Bars) + kMaskBytes;  // [2 warps][256]
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = uniform(tid >> 5);
   if (tid == 0) {
@@ -277,10 +305,18 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     mbar_init(&br->drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&br->sfull[i], 1);
-      mbar_init(&br->pready[i], 4);
+      mbar_init(&br->pready[i][0], 4);
+      mbar_init(&br->pready[i][1], 4);
       mbar_init(&br->pvdone[i], 1);
     }
-    for (int i = 0; i < kFixRing; ++i) mbar_init(&br->fixed[i], 2);
+    for (int i = 0; i < kFixRing; ++i) {
+      mbar_init(&br->partfull[i], 1);
+      mbar_init(&br->fixed[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&br->maskfull[i], 2);
+      mbar_init(&br->maskempty[i], 8);
+    }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&br->segfull[i], 1);
       mbar_init(&br->segempty[i], 1 + 8 + 2);
@@ -290,6 +326,10 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     br->where = -1;
   }
   if (warp == kMmaWarp) tmem_alloc(&br->tmem, kTmemCols);
+  if (tid >= kCopyWarp * 32 && tid < kCopyWarp * 32 + (PAGED ? 5 : 3)) {
+    const CUtensorMap* maps[5] = {qmap, kmap, vmap, kpmap, vpmap};
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[lane])) : "memory");
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -301,16 +341,16 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
   if (warp == kCopyWarp) {
     // ---------------- work list and copies
     W work(a);
-    uint32_t cnt = 0;  // key and value tiles requested
+    uint32_t cnt = 0, fix = 0;  // key and value tiles requested; values to be made safe
     int n_q = 0;       // items whose queries were requested
     auto slot_free = [&](uint32_t c) -> bool {
-      return c < NS || mbar_wait_suspend(&br->kvempty[c % NS], ((c / NS) - 1) & 1, abort);
+      return c < NS || wait_bar(&br->kvempty[c % NS], ((c / NS) - 1) & 1, abort);
     };
     int n = 0;
     Seg s;
     for (; ok; ++n) {
       const int r = n % kRing;
-      if (n >= kRing) ok = mbar_wait_suspend(&br->segempty[r], ((n / kRing) - 1) & 1, abort);
+      if (n >= kRing) ok = wait_bar(&br->segempty[r], ((n / kRing) - 1) & 1, abort);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const bool more = work.next(s);
       if (!more) s.b = -1;
@@ -334,6 +374,14 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       int page = page_of(s.u0);
       auto load = [&](int u, bool val, int pg) {
         uint64_t* bar = &br->kvfull[cnt % NS];
+        int lim;
+        bool by_row;
+        if (val && tile_part<PAGED>(s, u, lim, by_row)) {
+          // lands on a barrier of the warps that make it safe (they see only such tiles, in
+          // turn, and the ring cannot pass one by); the products wait for those warps
+          if (lane == 0) mbar_arrive(bar);
+          bar = &br->partfull[fix++ % kFixRing];
+        }
         uint8_t* dst = smem + L::kOffKV + (cnt % NS) * L::kTile;
         if (PAGED && u < s.npre) {
           const CUtensorMap* m = val ? vpmap : kpmap;
@@ -378,7 +426,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         load(u, false, page);
         if (u == s.u0) {  // the queries, once the previous item's score products are done
-          if (n > 0) ok = mbar_wait_suspend(&br->qempty, (n - 1) & 1, abort);
+          if (n > 0) ok = wait_bar(&br->qempty, (n - 1) & 1, abort);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           ++n_q;
           if (lane == 0) {
@@ -402,6 +450,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       if (lane == 0) br->where = s.b;
       for (uint32_t c = cnt > NS ? cnt - NS : 0; c < cnt; ++c)
         (void)mbar_wait(&br->kvfull[c % NS], (c / NS) & 1);
+      for (uint32_t c = fix > kFixRing ? fix - kFixRing : 0; c < fix; ++c)
+        (void)mbar_wait(&br->partfull[c % kFixRing], (c / kFixRing) & 1);
       if (n_q > 0) (void)mbar_wait(&br->qfull, (n_q - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
@@ -417,7 +467,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     const uint32_t dK = (smem_addr(smem + L::kOffKV) >> 4) | (1u << 16);
     const uint32_t dV = (smem_addr(smem + L::kOffKV) >> 4) | ((uint32_t)(L::kHalf >> 4) << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort)) != 0;
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, abort)) != 0;
     };
     auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
       // the previous O_t += P_t V has read P_t, which lies in S_t's columns
@@ -433,16 +483,22 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       commit(&br->sfull[t]);
       return true;
     };
-    auto pv = [&](int t, uint32_t c, bool first) {  // O_t (+)= P_t V of the tile in slot c
-      tc_fence_after_sync();
+    // O_t (+)= P_t V of the tile in slot c, 64 keys at a time as their P comes
+    auto pv = [&](int t, uint32_t c, bool first) -> bool {
       const uint32_t slot = c % NS;
       const uint32_t v = dV + slot * (L::kTile >> 4);
       const uint32_t add = first ? 0u : 1u;
 #pragma unroll
-      for (int i = 0; i < kKeys / 16; ++i)
-        mma_ts(utm + 256 + t * 128, utm + t * 128 + i * 8, v + i * 128, id_o,
-               i > 0 ? 1u : add);
+      for (int h = 0; h < 2; ++h) {
+        if (!wait(&br->pready[t][h], done[t] & 1)) return false;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int i = h * 4; i < h * 4 + 4; ++i)
+          mma_ts(utm + 256 + t * 128, utm + t * 128 + i * 8, v + i * 128, id_o, i > 0 ? 1u : add);
+      }
       commit(&br->pvdone[t]);
+      ++done[t];
+      return true;
     };
     for (int n = 0; ok; ++n) {
       const int r = n % kRing;
@@ -464,27 +520,16 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         const uint32_t cv = cnt + 1, ck = cnt + 2;  // this value tile, the next key tile
         const bool x0 = u < s.e0, x1 = u < s.e1;    // steps of the row tiles
         const bool y0 = u + 1 < s.e0, y1 = u + 1 < s.e1;
-        if (x0) ok = wait(&br->pready[0], done[0] & 1);
-        if (ok) ok = wait(&br->kvfull[cv % NS], (cv / NS) & 1);
+        ok = wait(&br->kvfull[cv % NS], (cv / NS) & 1);
         int lim;
         bool by_row;
         if (ok && tile_part<PAGED>(s, u, lim, by_row)) {
           ok = wait(&br->fixed[fix % kFixRing], (fix / kFixRing) & 1);
           ++fix;
         }
-        if (!ok) break;
-        if (x0) {
-          pv(0, cv, u == s.u0);
-          ++done[0];
-        }
-        if (y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
-        if (ok && x1) {
-          ok = wait(&br->pready[1], done[1] & 1);
-          if (ok) {
-            pv(1, cv, u == s.u0);
-            ++done[1];
-          }
-        }
+        if (ok && x0) ok = pv(0, cv, u == s.u0);
+        if (ok && y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
+        if (ok && x1) ok = pv(1, cv, u == s.u0);
         if (!ok) break;
         commit(&br->kvempty[cv % NS]);
         if (y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
@@ -510,22 +555,51 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     const int ft = tid - kFixWarp * 32;  // 0 .. 63
     W::first(a, ft);  // status words, outputs of sequences that have no work
     uint32_t cnt = 0, fix = 0;
+    int built = 0;
     for (int n = 0; ok; ++n) {
       const int r = n % kRing;
-      ok = mbar_wait_suspend(&br->segfull[r], (n / kRing) & 1, abort);
+      ok = wait_bar(&br->segfull[r], (n / kRing) & 1, abort);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const Seg s = br->seg[r];
       if (s.b < 0) break;
-      for (int u = s.u0; ok && u < s.u1; ++u, cnt += 2) {
-        // every tile is awaited in turn, also those left alone: a barrier two phases back
-        // would pass for done
-        const uint32_t cv = cnt + 1;
-        ok = mbar_wait_suspend(&br->kvfull[cnt % NS], (cnt / NS) & 1, abort) &&
-             mbar_wait_suspend(&br->kvfull[cv % NS], (cv / NS) & 1, abort);
+      if (PAGED && s.u1 > s.npre) {
+        // The ancestor-or-self sets of the item's nodes, ahead of the softmax warps that come
+        // to the tree's tiles last: the mask of a node's topological position names positions,
+        // the order (staged as bytes, a copy per warp) turns them into nodes.
+        const int k = built++;
+        if (k >= 2) ok = wait_bar(&br->maskempty[k & 1], ((k >> 1) - 1) & 1, abort);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        uint8_t* ord = sord + (warp - kFixWarp) * kMaxNodes;
+        __syncwarp();
+        for (int i = lane; i < s.N; i += 32) ord[i] = (uint8_t)a.order[s.lo + i];
+        __syncwarp();
+        for (int i = ft; i < 2 * a.tpt && s.tok0 + i < s.N; i += 64) {
+          uint32_t* m = smask + ((k & 1) * 2 * kRows + i) * kMaskWords;
+          const int p = a.pos[s.lo + s.tok0 + i];
+          uint64_t anc[kMaxNodes / 64];
+#pragma unroll
+          for (int w = 0; w < kMaxNodes / 64; ++w) {
+            anc[w] = w < a.words && p >= 0 && p < s.N ? a.anc[(int64_t)(s.lo + p) * a.words + w] : 0;
+            m[2 * w] = m[2 * w + 1] = 0;
+          }
+#pragma unroll
+          for (int w = 0; w < kMaxNodes / 64; ++w)
+            for (uint64_t bits = anc[w]; bits; bits &= bits - 1) {
+              const int bp = w * 64 + __ffsll(static_cast<long long>(bits)) - 1;
+              if (bp >= s.N) break;
+              m[ord[bp] >> 5] |= 1u << (ord[bp] & 31);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br->maskfull[k & 1]);
+      }
+      for (int u = s.u0; ok && u < s.u1; ++u, cnt += 2) {
         int lim;
         bool by_row;
         if (!tile_part<PAGED>(s, u, lim, by_row)) continue;
+        const uint32_t cv = cnt + 1;
+        ok = wait_bar(&br->partfull[fix % kFixRing], (fix / kFixRing) & 1, abort);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + L::kOffKV + (cv % NS) * L::kTile);
         uint32_t acc = 0;
         for (int i = ft; i < L::kTile / 16; i += 64) {
@@ -567,10 +641,11 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     const float c2 = a.scale * 1.4426950408889634f;
     const float gap = kGap / a.scale;
     const int tok_in = row / a.G, g = row - tok_in * a.G;
-    uint32_t done = 0, built = 0;
+    uint32_t done = 0;
+    int built = 0;
     for (int n = 0; ok; ++n) {
       const int r = n % kRing;
-      ok = mbar_wait_suspend(&br->segfull[r], (n / kRing) & 1, abort);
+      ok = wait_bar(&br->segfull[r], (n / kRing) & 1, abort);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const Seg s = br->seg[r];
       if (s.b < 0) break;
@@ -578,41 +653,11 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       if (e > s.u0) {
         const int tok = s.tok0 + t * a.tpt + tok_in;
         const bool live = tok_in < a.tpt && tok < s.N;
-        uint32_t mask[kMaxNodes / 32];  // (paged)
-        if constexpr (PAGED) {
-          // ancestor-or-self set in node-index space, from the topological order (staged as
-          // bytes) and the mask of the node's position; only where the tree's tiles come
-#pragma unroll
-          for (int w = 0; w < kMaxNodes / 32; ++w) mask[w] = 0;
-          if (e > s.npre) {
-            // every warp writes the whole copy (the same bytes), so none waits for another;
-            // two copies in turn: a warp gets to the copy after next only past products that
-            // all four warps fed
-            uint8_t* ord = sord + (t * 2 + (built & 1)) * kMaxNodes;
-            ++built;
-            for (int i = lane; i < s.N; i += 32) ord[i] = (uint8_t)a.order[s.lo + i];
-            __syncwarp();
-            const int p = live ? a.pos[s.lo + tok] : -1;
-            if (p >= 0 && p < s.N) {
-              for (int w = 0; w < a.words; ++w) {
-                uint64_t bits = a.anc[(int64_t)(s.lo + p) * a.words + w];
-                while (bits) {
-                  const int bp = w * 64 + __ffsll(static_cast<long long>(bits)) - 1;
-                  bits &= bits - 1;
-                  if (bp >= s.N) break;
-                  const int x = ord[bp];
-#pragma unroll
-                  for (int j = 0; j < kMaxNodes / 32; ++j)
-                    if ((x >> 5) == j) mask[j] |= 1u << (x & 31);
-                }
-              }
-            }
-          }
-        }
+        const uint32_t* mask = smask + ((built & 1) * 2 * kRows + t * a.tpt + tok_in) * kMaskWords;
         float m = -INFINITY;
         float2 la = make_float2(0.f, 0.f), lb = la;  // the row's sum, in four parts
         for (int u = s.u0; u < e; ++u) {
-          ok = mbar_wait_suspend(&br->sfull[t], done & 1, abort);
+          ok = wait_bar(&br->sfull[t], done & 1, abort);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after_sync();
           float x[kKeys];
@@ -623,14 +668,15 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           // masks
           if constexpr (PAGED) {
             if (u >= s.npre) {
-              const int w0 = (u - s.npre) * 4;
+              if (u == max(s.u0, s.npre)) ok = wait_bar(&br->maskfull[built & 1], (built >> 1) & 1, abort);
+              if (!(ok = __all_sync(0xffffffffu, ok))) break;
+              const uint4 w4 = reinterpret_cast<const uint4*>(mask)[u - s.npre];
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t w = w0 == 0 ? mask[q] : mask[4 + q];
+              for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
-                  if (!((w >> c) & 1u)) x[q * 32 + c] = -INFINITY;
-              }
+                  if (!((w[q] >> c) & 1u)) x[q * 32 + c] = -INFINITY;
             } else if (s.P - u * kKeys < kKeys) {
               const int lim = s.P - u * kKeys;
 #pragma unroll
@@ -685,15 +731,17 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
               w[c] = Elem<E>::pack(y.x, y.y);
             }
             tmem_st16(tS + q * 16, w);
+            if (q & 1) {  // 64 keys are ready
+              tmem_st_wait();
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&br->pready[t][q >> 1]);
+            }
           }
-          tmem_st_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&br->pready[t]);
           ++done;
         }
         // the item's last product on O_t
-        if (ok) ok = mbar_wait_suspend(&br->pvdone[t], (done - 1) & 1, abort);
+        if (ok) ok = wait_bar(&br->pvdone[t], (done - 1) & 1, abort);
         if (!(ok = __all_sync(0xffffffffu, ok))) {
           if (lane == 0) br->where = s.b;
           break;
@@ -705,48 +753,55 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         const float inv = l == 0.f ? 0.f : 1.f / l;
         E* orow = static_cast<E*>(a.o) + (int64_t)(s.lo + tok) * a.o_stride +
                   (int64_t)(s.hk * a.G + g) * a.d;
-        float* prow = nullptr;
-        if (PAGED && s.part >= 0 && live)
-          prow = a.part + ((int64_t)(blockIdx.x * 2 + s.part) * a.part_rows + t * kRows + row) *
-                              part_stride<DP>();
+        const bool cut = PAGED && s.part >= 0;
+        const int64_t slot = blockIdx.x * 2 + (cut ? s.part : 0);
 #pragma unroll 1
-        for (int q = 0; q < DP / 16; ++q) {
-          float o[16];
-          tmem_ld16(tO + q * 16, o);
-          tmem_ld_wait();
-          if (dirty && live) {
-            uint32_t seen[kMaxNodes / 32];
-#pragma unroll
-            for (int w = 0; w < kMaxNodes / 32; ++w) seen[w] = PAGED ? mask[w] : 0;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (q * 16 + c < a.d)
-                o[c] += nonfinite_sum<E, PAGED>(&a, &br->seg[r], tok, seen, q * 16 + c);
-          }
+        for (int q = 0; q < DP / 32; ++q) {
+          float o[32];
+          tmem_ld32(tO + q * 32, o);
+          ld_wait32(o);
           if (!live) continue;
-          if (prow != nullptr) {
+          if (dirty) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<float4*>(prow + q * 16 + c * 4) =
+            for (int c = 0; c < 32; ++c)
+              if (q * 32 + c < a.d)
+                o[c] += nonfinite_sum<E, PAGED>(&a, &br->seg[r], tok, mask, q * 32 + c);
+          }
+          if (cut) {  // column groups of four, rows side by side
+            float4* part = reinterpret_cast<float4*>(a.part) +
+                           (slot * (DP / 4) + q * 8) * a.part_rows + t * kRows + row;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              part[(int64_t)c * a.part_rows] =
                   make_float4(o[c * 4], o[c * 4 + 1], o[c * 4 + 2], o[c * 4 + 3]);
           } else {
-            const float f = bad ? 0.f : inv;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              if (q * 16 + c * 8 >= a.d) continue;
-              uint32_t w[4];
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = bad ? 0u : Elem<E>::pack(o[c * 8 + 2 * i] * f, o[c * 8 + 2 * i + 1] * f);
-              *reinterpret_cast<uint4*>(orow + q * 16 + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 8; ++i)
+                w[i] = bad ? 0u : Elem<E>::pack(o[c * 16 + 2 * i] * inv, o[c * 16 + 2 * i + 1] * inv);
+              E* to = orow + q * 32 + c * 16;
+              const int left = a.d - (q * 32 + c * 16);
+              if (a.o_wide && left >= 16) {
+                st_global32(to, w);
+              } else {
+                if (left > 0) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (left > 8) *reinterpret_cast<uint4*>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
             }
           }
         }
-        if (prow != nullptr) {
-          prow[DP] = m == -INFINITY ? 0.f : m * c2;
-          prow[DP + 1] = l;
-        }
+        if (cut && live)
+          a.part_ml[slot * a.part_rows + t * kRows + row] =
+              make_float2(m == -INFINITY ? 0.f : m * c2, l);
         tc_fence_before_sync();
+      }
+      if (PAGED && s.u1 > s.npre) {  // done with the item's masks
+        ok = wait_bar(&br->maskfull[built & 1], (built >> 1) & 1, abort);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) mbar_arrive(&br->maskempty[built & 1]);
+        ++built;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&br->segempty[r]);

@@ -34,7 +34,7 @@ __device__ __forceinline__ Plan plan_of(const Args& a, int b) {
   // (words this kernel itself may write count as planned: every CTA plans the same work)
   const bool run = p.st == TGDN_SEQ_OK || p.st == TGDN_SEQ_TIMEOUT || p.st == TGDN_SEQ_BAD_PAGE;
   if (!run || p.lo < 0 || p.N <= 0 || hi > a.T || p.N > a.n_max || p.P < 0 || held < 0 ||
-      held > a.max_pages || p.P > (int64_t)held * a.ps)
+      held > a.max_pages || p.P > (int64_t)held * a.ps || (p.P > 0 && a.n_pages == 0))
     return p;  // nt = 0
   p.npre = (p.P + kKeys - 1) / kKeys;
   p.nt = p.npre + (p.N + kKeys - 1) / kKeys;
@@ -43,6 +43,12 @@ __device__ __forceinline__ Plan plan_of(const Args& a, int b) {
 __device__ __forceinline__ int64_t items_of(const Args& a, const Plan& p) {
   const int blk = a.tpt * 2;
   return p.nt ? (int64_t)((p.N + blk - 1) / blk) * a.H_kv : 0;
+}
+
+// Quotient of non-negative numbers (nearly always small ones, which divide faster).
+__device__ __forceinline__ int64_t divide(int64_t n, int64_t by) {
+  if ((n | by) >> 32 == 0) return (uint32_t)n / (uint32_t)by;
+  return n / by;
 }
 
 __device__ __forceinline__ int64_t warp_sum_upto(int64_t v, int lane) {
@@ -56,19 +62,36 @@ __device__ __forceinline__ int64_t warp_sum_upto(int64_t v, int lane) {
 
 struct PagedWork {
   const Args& a;
-  int lane, chunk = 0, n = 0;
-  int64_t before = 0, x, x1, share;
+  int lane, n = 0;
+  int64_t x, x1, share;
   int4 d0, d1;
+  // the 32 sequences from `chunk` on (a lane each): their tiles before them and in them
+  int chunk = 0;
+  Plan p;
+  int64_t before = 0, tiles, upto, total;
 
+  __device__ void load(int c) {
+    chunk = c;
+    p = Plan{};
+    if (c + lane < a.B) p = plan_of(a, c + lane);
+    tiles = items_of(a, p) * p.nt;
+    upto = warp_sum_upto(tiles, lane);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+  }
   __device__ explicit PagedWork(const Args& args) : a(args), lane(threadIdx.x & 31) {
-    int64_t sum = 0;
-    for (int b = lane; b < a.B; b += 32) {
-      const Plan p = plan_of(a, b);
-      sum += items_of(a, p) * p.nt;
+    // (a call that ends early must leave nothing for the merge to read)
+    if (a.part != nullptr && lane == 0) a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    load(0);
+    int64_t sum = total;
+    if (a.B > 32) {
+      int64_t more = 0;
+      for (int b = 32 + lane; b < a.B; b += 32) {
+        const Plan q = plan_of(a, b);
+        more += items_of(a, q) * q.nt;
+      }
+      sum += __shfl_sync(0xffffffffu, warp_sum_upto(more, lane), 31);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    share = (sum + gridDim.x - 1) / gridDim.x;
+    share = divide(sum + gridDim.x - 1, gridDim.x);
     if (share < kMinShare) share = kMinShare;
     x = min(sum, share * blockIdx.x);
     x1 = min(sum, x + share);
@@ -91,14 +114,10 @@ struct PagedWork {
 
   __device__ bool next(Seg& s) {
     while (x < x1) {
-      for (;; chunk += 32) {
-        Plan p{};
-        if (chunk + lane < a.B) p = plan_of(a, chunk + lane);
-        const int64_t tiles = items_of(a, p) * p.nt;
-        const int64_t upto = warp_sum_upto(tiles, lane);
-        const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+      for (;;) {
         if (x >= before + total) {
           before += total;
+          load(chunk + 32);
           continue;
         }
         const int64_t at = x - before;
@@ -111,10 +130,10 @@ struct PagedWork {
         s.npre = __shfl_sync(0xffffffffu, p.npre, f);
         const int nt = __shfl_sync(0xffffffffu, p.nt, f);
         s.zero = __shfl_sync(0xffffffffu, p.st, f) != TGDN_SEQ_OK;
-        const int item = (int)(in / nt);
+        const int item = (int)divide(in, nt);
         s.hk = item % a.H_kv;
         s.tok0 = item / a.H_kv * a.tpt * 2;
-        s.u0 = (int)(in % nt);
+        s.u0 = (int)(in - (int64_t)item * nt);
         const int64_t x_item = x - s.u0;
         if (a.part == nullptr) {
           x = x_item + nt;
@@ -129,7 +148,7 @@ struct PagedWork {
         s.e1 = s.tok0 + a.tpt < s.N ? s.u1 : 0;
         if (s.u0 == 0 && s.u1 < nt) {
           d0 = make_int4(s.b, s.lo, s.N, s.tok0);
-          d1 = make_int4(s.hk, (int)((x_item + nt - 1) / share), s.part, 0);
+          d1 = make_int4(s.hk, (int)divide(x_item + nt - 1, share), s.part, 0);
         }
         ++n;
         return true;
@@ -157,70 +176,79 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x's run and goes on into later
-// ones: a warp per query row.
+// ones, 32 query rows per CTA: a thread holds four columns (or a few times four) of one row.
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
+constexpr int kMergeRows = 32;
 template <int DP, typename E>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ Args a) {
+  __shared__ __align__(16) uint8_t s_out[kMergeRows][DP * 2 + 16];
   grid_dependency_wait();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, tid = threadIdx.x;
   const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
   if (d0.x < 0) return;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (r >= a.part_rows) return;
-  const int t = r / kRows, row = r % kRows, tok_in = row / a.G;
-  const int tok = d0.w + t * a.tpt + tok_in;
-  if (tok_in >= a.tpt || tok >= d0.z) return;
-  constexpr int V = DP / 32;  // columns per lane
-  const int64_t slot = (int64_t)a.part_rows * part_stride<DP>();
-  const float* own = a.part + (2 * c + d1.z) * slot + (int64_t)r * part_stride<DP>();
-  const float* rest = a.part + (int64_t)r * part_stride<DP>();
-  auto row_of = [&](int i) { return i == c ? own : rest + 2 * i * slot; };
-  float M = -INFINITY;
-  for (int i = c + lane; i <= d1.y; i += 32) {
-    const float* p = row_of(i);
-    if (p[DP + 1] != 0.f) M = fmaxf(M, p[DP]);
-  }
+  const int r0 = blockIdx.y * kMergeRows, R = min(kMergeRows, a.part_rows - r0);
+  if ((r0 / kRows) * a.tpt + d0.w >= d0.z) return;  // no row of this row tile exists
+  int rp = 1;  // threads side by side over rows: the power of two from R up
+  while (rp < R) rp *= 2;
+  const int r = tid & (rp - 1), cg0 = tid / rp, step = 256 / rp;
+  constexpr int C = DP / 4, kPer = C / 8;  // column groups; the most of one thread
+  float M = -INFINITY, sum = 0.f;
+  float4 acc[kPer];
 #pragma unroll
-  for (int o = 16; o >= 1; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float sum = 0.f, acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int k = 0; k < kPer; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // part i lies in CTA i's first slot, the first part in the slot its CTA named
+  auto slot = [&](int i) -> int64_t { return 2 * i + (i == c ? d1.z : 0); };
+  if (r < R && cg0 < C) {
+    const float2* ml = a.part_ml + r0 + r;
+    const float4* part = reinterpret_cast<const float4*>(a.part) + r0 + r;
 #pragma unroll 4
-  for (int i = c; i <= d1.y; ++i) {
-    const float* p = row_of(i);
-    const float l = p[DP + 1];
-    const float w = l == 0.f ? 0.f : fast_exp2(p[DP] - M);
-    sum = fmaf(w, l, sum);
-    float x[V];
-    if (V == 4) {
-      const float4 y = reinterpret_cast<const float4*>(p)[lane];
-      x[0] = y.x, x[1] = y.y, x[V - 2] = y.z, x[V - 1] = y.w;
-    } else {
-      const float2 y = reinterpret_cast<const float2*>(p)[lane];
-      x[0] = y.x, x[1] = y.y;
+    for (int i = c; i <= d1.y; ++i) {
+      const float2 v = ml[slot(i) * a.part_rows];
+      if (v.y != 0.f) M = fmaxf(M, v.x);
     }
+#pragma unroll 4
+    for (int i = c; i <= d1.y; ++i) {
+      const float2 v = ml[slot(i) * a.part_rows];
+      const float w = v.y == 0.f ? 0.f : fast_exp2(v.x - M);
+      sum = fmaf(w, v.y, sum);
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[v], acc[v]);
+      for (int k = 0; k < kPer; ++k) {
+        if (cg0 + k * step >= C) continue;
+        const float4 o = part[(slot(i) * C + cg0 + k * step) * a.part_rows];
+        if (w != 0.f) {
+          acc[k].x = fmaf(w, o.x, acc[k].x);
+          acc[k].y = fmaf(w, o.y, acc[k].y);
+          acc[k].z = fmaf(w, o.z, acc[k].z);
+          acc[k].w = fmaf(w, o.w, acc[k].w);
+        }
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (cg0 + k * step < C)
+        *reinterpret_cast<uint2*>(&s_out[r][(cg0 + k * step) * 8]) =
+            make_uint2(Elem<E>::pack(acc[k].x * inv, acc[k].y * inv),
+                       Elem<E>::pack(acc[k].z * inv, acc[k].w * inv));
   }
+  __syncthreads();
   const bool ok = a.status[d0.x] == TGDN_SEQ_OK;
-  const float inv = !ok || sum == 0.f ? 0.f : 1.f / sum;
-  if (lane * V >= a.d) return;
-  E* orow = static_cast<E*>(a.o) + (int64_t)(d0.y + tok) * a.o_stride +
-            (int64_t)(d1.x * a.G + row % a.G) * a.d + lane * V;
-  uint32_t w[2];
-#pragma unroll
-  for (int v = 0; v < V / 2; ++v)
-    w[v] = ok ? Elem<E>::pack(acc[2 * v] * inv, acc[2 * v + 1] * inv) : 0u;
-  if (V == 4)
-    *reinterpret_cast<uint2*>(orow) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(orow) = w[0];
+  const int pieces = a.d / 8;  // 16-byte pieces of a row
+  for (int e = tid; e < R * pieces; e += 256) {
+    const int i = e / pieces, x = e - i * pieces;
+    const int rr = r0 + i, t = rr / kRows, row = rr % kRows, tok_in = row / a.G;
+    const int tok = d0.w + t * a.tpt + tok_in;
+    if (tok_in >= a.tpt || tok >= d0.z) continue;
+    E* to = static_cast<E*>(a.o) + (int64_t)(d0.y + tok) * a.o_stride +
+            (int64_t)(d1.x * a.G + row - tok_in * a.G) * a.d + x * 8;
+    *reinterpret_cast<uint4*>(to) =
+        ok ? *reinterpret_cast<const uint4*>(&s_out[i][x * 16]) : make_uint4(0, 0, 0, 0);
+  }
 }
 
 struct Split {
   int grid, rows;
-  size_t part_off, bytes;
+  size_t part_off, ml_off, bytes;
 };
 static Split split_of(int n_max, int G, int d) {
   Split p;
@@ -228,7 +256,8 @@ static Split split_of(int n_max, int G, int d) {
   p.grid = device_sm_count();
   p.rows = n_max <= tpt ? n_max * G : 2 * kRows;
   p.part_off = ((size_t)p.grid * 2 * sizeof(int4) + 255) / 256 * 256;
-  p.bytes = p.part_off + (size_t)p.grid * 2 * p.rows * (dp + 4) * sizeof(float);
+  p.ml_off = p.part_off + (size_t)p.grid * 2 * p.rows * dp * sizeof(float);
+  p.bytes = p.ml_off + (size_t)p.grid * 2 * p.rows * sizeof(float2);
   return p;
 }
 
@@ -242,7 +271,7 @@ static cudaError_t launch(const Args& a, int grid, const CUtensorMap& q, const C
   if (e != cudaSuccess) return e;
   e = launch_after(kern, dim3(grid), dim3(kBlock), smem, s, q, k, v, kp, vp, a);
   if (e != cudaSuccess || a.part == nullptr) return e;
-  return launch_after(paged_merge_kernel<DP, E>, dim3(grid, (a.part_rows + 7) / 8), dim3(256), 0, s,
+  return launch_after(paged_merge_kernel<DP, E>, dim3(grid, (a.part_rows + kMergeRows - 1) / kMergeRows), dim3(256), 0, s,
                       a);
 }
 
@@ -273,6 +302,7 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   a.status = t.status;
   a.o = o;
   a.o_stride = o_stride;
+  a.o_wide = wide_rows(o, o_stride, d);
   a.v = v_rows;
   a.v_stride = v_stride;
   a.n_max = t.n_max;
@@ -291,6 +321,7 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   if (ws != nullptr && ws_bytes >= p.bytes) {
     a.desc = static_cast<int4*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml_off);
   }
   if (d > 64)
     return io == TGDN_BF16 ? launch<128, __nv_bfloat16>(a, p.grid, q, k, v, kp, vp, s)

@@ -115,6 +115,7 @@ cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, f
   a.status = status;
   a.o = o;
   a.o_stride = o_stride;
+  a.o_wide = wide_rows(o, o_stride, d);
   a.v = v_rows;
   a.v_stride = v_stride;
   // at most T / blk + B blocks per head; one row tile per item when two would leave SMs idle
