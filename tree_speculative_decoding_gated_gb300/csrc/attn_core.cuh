@@ -83,9 +83,8 @@ struct Args {
   const void* v;                   // new rows' values (prompt or tree), for the rare exact path
   int64_t v_stride;
   // paged
-  int n_max, words, ps, n_pages, max_pages;
-  const int32_t *order, *pos, *table, *len, *held;
-  const uint64_t* anc;
+  int n_max, ps, n_pages, max_pages;
+  const int32_t *parent, *table, *len, *held;
   int tiles;                       // row tiles per item: 2, or 1 when items are few
   // partial results (null: items are never split): [slot][DP / 4][part_rows] float4 of O
   // unnormalised, [slot][part_rows] of (reference maximum in log2 units, sum)
@@ -230,14 +229,14 @@ struct alignas(16) Bars {
 };
 
 // Paged: ancestor-or-self sets of an item's nodes (node-index space), two items' worth, and a
-// byte copy of the topological order for each warp that builds them.
+// copy of the parents for each warp that builds them.
 constexpr int kMaskWords = kMaxNodes / 32;
 constexpr int kMaskBytes = 2 * 2 * kRows * kMaskWords * 4;
 static_assert(sizeof(Bars) % 16 == 0, "the masks behind it are read 16 bytes at a time");
 
 template <int DP, bool PAGED>
 constexpr int smem_bytes() {
-  return Lay<DP, PAGED>::kOffMisc + (int)sizeof(Bars) + (PAGED ? kMaskBytes + 2 * kMaxNodes : 0) + 1024;
+  return Lay<DP, PAGED>::kOffMisc + (int)sizeof(Bars) + (PAGED ? kMaskBytes + 4 * kMaxNodes : 0) + 1024;
 }
 static_assert(smem_bytes<128, true>() <= 227 * 1024, "fits one CTA per SM");
 
@@ -292,7 +291,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
   constexpr int NS = L::kStages;
   Bars* br = reinterpret_cast<Bars*>(smem + L::kOffMisc);
   uint32_t* smask = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + sizeof(Bars));  // [2][256][8]
-  uint8_t* sord = smem + L::kOffMisc + sizeof(Bars) + kMaskBytes;  // [2 warps][256]
+  uint16_t* spar = reinterpret_cast<uint16_t*>(smem + L::kOffMisc + sizeof(Bars) + kMaskBytes);  // [2][256]
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = uniform(tid >> 5);
   if (tid == 0) {
@@ -553,7 +552,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
   } else if (warp >= kFixWarp) {
     // ---------------- value rows that must not reach the product
     const int ft = tid - kFixWarp * 32;  // 0 .. 63
-    W::first(a, ft);  // status words, outputs of sequences that have no work
+    W::first(a, ft);  // status words
     uint32_t cnt = 0, fix = 0;
     int built = 0;
     for (int n = 0; ok; ++n) {
@@ -563,32 +562,29 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       const Seg s = br->seg[r];
       if (s.b < 0) break;
       if (PAGED && s.u1 > s.npre) {
-        // The ancestor-or-self sets of the item's nodes, ahead of the softmax warps that come
-        // to the tree's tiles last: the mask of a node's topological position names positions,
-        // the order (staged as bytes, a copy per warp) turns them into nodes.
+        // The ancestor-or-self sets of the item's nodes, ahead of the softmax warps (they come
+        // to the tree's tiles last): each lane walks up from a node, in a copy of the parents.
         const int k = built++;
         if (k >= 2) ok = wait_bar(&br->maskempty[k & 1], ((k >> 1) - 1) & 1, abort);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        uint8_t* ord = sord + (warp - kFixWarp) * kMaxNodes;
+        uint16_t* par = spar + (warp - kFixWarp) * kMaxNodes;
         __syncwarp();
-        for (int i = lane; i < s.N; i += 32) ord[i] = (uint8_t)a.order[s.lo + i];
+        for (int i = lane; i < s.N; i += 32) par[i] = (uint16_t)a.parent[s.lo + i];
         __syncwarp();
         for (int i = ft; i < 2 * a.tpt && s.tok0 + i < s.N; i += 64) {
-          uint32_t* m = smask + ((k & 1) * 2 * kRows + i) * kMaskWords;
-          const int p = a.pos[s.lo + s.tok0 + i];
-          uint64_t anc[kMaxNodes / 64];
+          uint64_t m[kMaxNodes / 64];
 #pragma unroll
-          for (int w = 0; w < kMaxNodes / 64; ++w) {
-            anc[w] = w < a.words && p >= 0 && p < s.N ? a.anc[(int64_t)(s.lo + p) * a.words + w] : 0;
-            m[2 * w] = m[2 * w + 1] = 0;
+          for (int w = 0; w < kMaxNodes / 64; ++w) m[w] = 0;
+          int x = s.tok0 + i;
+          for (int up = 0; up <= TGDN_MAX_DEPTH && x < s.N; ++up) {  // (the root's parent: 0xffff)
+#pragma unroll
+            for (int w = 0; w < kMaxNodes / 64; ++w)
+              if ((x >> 6) == w) m[w] |= 1ull << (x & 63);
+            x = par[x];
           }
+          uint64_t* out = reinterpret_cast<uint64_t*>(smask + ((k & 1) * 2 * kRows + i) * kMaskWords);
 #pragma unroll
-          for (int w = 0; w < kMaxNodes / 64; ++w)
-            for (uint64_t bits = anc[w]; bits; bits &= bits - 1) {
-              const int bp = w * 64 + __ffsll(static_cast<long long>(bits)) - 1;
-              if (bp >= s.N) break;
-              m[ord[bp] >> 5] |= 1u << (ord[bp] & 31);
-            }
+          for (int w = 0; w < kMaxNodes / 64; ++w) out[w] = m[w];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&br->maskfull[k & 1]);
@@ -632,6 +628,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&br->segempty[r]);
     }
+    W::last(a, ft);  // outputs of sequences that have no work
   } else {
     // ---------------- softmax: row tile t, one row per thread
     const int t = warp >> 2;

@@ -18,6 +18,7 @@ namespace tgdn {
 namespace attn {
 
 constexpr int kMinShare = 4;  // key tiles per CTA below which a cut costs more than it saves
+constexpr int kItemCost = 1;  // an item's start and output, in key tiles
 
 // Cached and tree key tiles of sequence b; 0: no work (empty, or an error).
 struct Plan {
@@ -74,7 +75,7 @@ struct PagedWork {
     chunk = c;
     p = Plan{};
     if (c + lane < a.B) p = plan_of(a, c + lane);
-    tiles = items_of(a, p) * p.nt;
+    tiles = items_of(a, p) * (p.nt + kItemCost);
     upto = warp_sum_upto(tiles, lane);
     total = __shfl_sync(0xffffffffu, upto, 31);
   }
@@ -87,7 +88,7 @@ struct PagedWork {
       int64_t more = 0;
       for (int b = 32 + lane; b < a.B; b += 32) {
         const Plan q = plan_of(a, b);
-        more += items_of(a, q) * q.nt;
+        more += items_of(a, q) * (q.nt + kItemCost);
       }
       sum += __shfl_sync(0xffffffffu, warp_sum_upto(more, lane), 31);
     }
@@ -100,7 +101,8 @@ struct PagedWork {
   }
 
   // Sequences without work but with rows: zeros, and the word for a bad length.
-  static __device__ void first(const Args& a, int ft) {
+  static __device__ void first(const Args&, int) {}
+  static __device__ void last(const Args& a, int ft) {
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       const Plan p = plan_of(a, b);
       if (p.nt || p.N <= 0 || p.st == TGDN_SEQ_BAD_RANGE || p.lo < 0 || p.lo + p.N > a.T) continue;
@@ -130,18 +132,18 @@ struct PagedWork {
         s.npre = __shfl_sync(0xffffffffu, p.npre, f);
         const int nt = __shfl_sync(0xffffffffu, p.nt, f);
         s.zero = __shfl_sync(0xffffffffu, p.st, f) != TGDN_SEQ_OK;
-        const int item = (int)divide(in, nt);
+        const int item = (int)divide(in, nt + kItemCost);
         s.hk = item % a.H_kv;
         s.tok0 = item / a.H_kv * a.tpt * 2;
-        s.u0 = (int)(in - (int64_t)item * nt);
-        const int64_t x_item = x - s.u0;
-        if (a.part == nullptr) {
-          x = x_item + nt;
-          if (s.u0 > 0) break;  // another CTA's
+        s.u0 = (int)(in - (int64_t)item * (nt + kItemCost));
+        const int64_t x_item = x - s.u0, x_next = x_item + nt + kItemCost;
+        if (a.part == nullptr || s.u0 >= nt) {
+          x = x_next;
+          if (s.u0 > 0) break;  // another CTA's item
           s.u1 = nt;
         } else {
           s.u1 = (int)min((int64_t)nt, s.u0 + (x1 - x));
-          x += s.u1 - s.u0;
+          x = min(x_next, x1);
         }
         s.part = s.u0 == 0 && s.u1 == nt ? -1 : (n == 0 ? 0 : 1);
         s.e0 = s.u1;
@@ -306,13 +308,10 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   a.v = v_rows;
   a.v_stride = v_stride;
   a.n_max = t.n_max;
-  a.words = t.words;
   a.ps = pg.page_size;
   a.n_pages = pg.n_pages;
   a.max_pages = pg.max_pages;
-  a.order = t.order;
-  a.pos = t.pos;
-  a.anc = t.anc;
+  a.parent = t.parent;
   a.table = pg.table;
   a.len = pg.len;
   a.held = pg.held;

@@ -27,6 +27,7 @@ struct PromptWork {
     for (int b = ft; b < a.B; b += 64)
       a.status[b] = valid(a, a.cu[b], a.cu[b + 1]) ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
   }
+  static __device__ void last(const Args&, int) {}
   __device__ bool next(Seg& s) {
     const int grid = gridDim.x, c = blockIdx.x;
     const int64_t x = (int64_t)turn * grid + ((turn & 1) ? grid - 1 - c : c);
