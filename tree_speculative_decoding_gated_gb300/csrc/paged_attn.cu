@@ -18,6 +18,7 @@ namespace tgdn {
 namespace attn {
 
 constexpr int kMinShare = 4;  // key tiles per CTA below which a cut costs more than it saves
+constexpr int kSplitTiles = 6;  // caches that can hold no more key tiles than this are never cut
 constexpr int kItemCost = 1;  // an item's start and output, in key tiles
 
 // Cached and tree key tiles of sequence b; 0: no work (empty, or an error).
@@ -317,7 +318,9 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   a.held = pg.held;
   const Split p = split_of(t.n_max, a.G, d);
   a.part_rows = p.rows;
-  if (ws != nullptr && ws_bytes >= p.bytes) {
+  // a short cache is not split: the merge would take longer than the tiles it spares
+  const int64_t most = ((int64_t)pg.max_pages * pg.page_size + kKeys - 1) / kKeys + (t.n_max + kKeys - 1) / kKeys;
+  if (ws != nullptr && ws_bytes >= p.bytes && most > kSplitTiles) {
     a.desc = static_cast<int4*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml_off);
