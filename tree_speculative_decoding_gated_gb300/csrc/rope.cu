@@ -15,6 +15,8 @@
 namespace tgdn {
 
 constexpr int kRopeThreads = 256;
+constexpr int kAhead = 4;
+constexpr int kRopeRows = 16;  // rows per CTA at most
 
 template <typename E> struct RopeIo;
 template <> struct RopeIo<float> {
@@ -69,34 +71,33 @@ template <> struct RopeIo<__half> {
   }
 };
 
-// The sequence of row t, or -1: the last b with cu[b] <= t, if its range is sound.
+// The sequence of row t, or -1: the last b with cu[b] <= t, if its range is sound.  Called
+// by a whole warp, which tests 32 offsets at a time.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int T, int t) {
-  int lo = 0, hi = B;  // cu[lo] <= t is kept where it holds at all
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= t) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int b = -1;
+  for (int c = 0; c < B; c += 32) {
+    const uint32_t below = __ballot_sync(0xffffffffu, c + lane < B && cu[c + lane] <= t);
+    if (below) b = c + 31 - __clz(below);
+    if (below != 0xffffffffu) break;
   }
-  const int c0 = cu[lo], c1 = cu[lo + 1];
-  return c0 >= 0 && c0 <= t && t < c1 && c1 <= T ? lo : -1;
+  if (b < 0) return -1;
+  const int c0 = cu[b], c1 = cu[b + 1];
+  return c0 >= 0 && t < c1 && c1 <= T ? b : -1;
 }
 
-// rows: rows per CTA.  PAIRED: the half layout with rot / 2 a multiple of the 16-byte piece,
-// so that a thread holds both pieces of its pairs; otherwise element by element.
-template <typename E>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int rows) {
-  extern __shared__ float2 turn[];  // [rows][rot / 2]: mscale (cos, sin)
-  constexpr int V = RopeIo<E>::V;
-  __shared__ int64_t s_pos[32];
-  __shared__ int s_ok[32];
-  const int tid = threadIdx.x, t0 = blockIdx.x * rows;
-  const int half = a.rot / 2;
-  if (tid < rows) {
-    const int t = t0 + tid;
+// The rows' positions (a warp per row) and their cosines and sines, to shared memory.
+__device__ __forceinline__ void rope_table(const RopeArgs& a, int t0, int rows, float2* turn,
+                                           int64_t* s_pos, int* s_ok) {
+  const int tid = threadIdx.x, half = a.rot / 2;
+  for (int r = tid >> 5; r < rows; r += kRopeThreads / 32) {
+    const int t = t0 + r;
     const int b = t < a.T ? sequence_of(a.cu, a.B, a.T, t) : -1;
-    s_ok[tid] = b >= 0;
-    if (b >= 0)
-      s_pos[tid] = (int64_t)(a.base ? a.base[b] : 0) + (a.off ? a.off[t] : t - a.cu[b]);
+    if ((tid & 31) == 0) {
+      s_ok[r] = b >= 0;
+      if (b >= 0)
+        s_pos[r] = (int64_t)(a.base ? a.base[b] : 0) + (a.off ? a.off[t] : t - a.cu[b]);
+    }
   }
   __syncthreads();
   for (int e = tid; e < rows * half; e += kRopeThreads) {
@@ -111,67 +112,120 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
     turn[e] = make_float2(c * a.mscale, s * a.mscale);
   }
   __syncthreads();
-  const int pieces = a.d / V, heads = a.H_q + a.H_kv;
-  auto row_in = [&](int r, int h) -> const E* {
-    const int64_t t = t0 + r;
-    return h < a.H_q ? static_cast<const E*>(a.q) + t * a.q_stride + (int64_t)h * a.d
-                     : static_cast<const E*>(a.k) + t * a.k_stride + (int64_t)(h - a.H_q) * a.d;
+}
+
+template <typename E>
+__device__ __forceinline__ const E* rope_in(const RopeArgs& a, int64_t t, int h) {
+  return h < a.H_q ? static_cast<const E*>(a.q) + t * a.q_stride + (int64_t)h * a.d
+                   : static_cast<const E*>(a.k) + t * a.k_stride + (int64_t)(h - a.H_q) * a.d;
+}
+template <typename E>
+__device__ __forceinline__ E* rope_out(const RopeArgs& a, int64_t t, int h) {
+  return h < a.H_q ? static_cast<E*>(a.q_out) + t * a.q_out_stride + (int64_t)h * a.d
+                   : static_cast<E*>(a.k_out) + t * a.k_out_stride + (int64_t)(h - a.H_q) * a.d;
+}
+
+// 16-byte pieces: a unit is one piece (interleaved pairs), or the two pieces of eight pairs
+// (halves), or one piece past rot that is copied.  A thread loads kAhead units at once, the
+// first ones before the rows' angles are known, so that the loads do not wait for them; the
+// unit, head and row advance by fixed steps instead of divisions.
+template <typename E, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int rows) {
+  extern __shared__ __align__(16) float2 turn[];  // [rows][rot / 2]: mscale (cos, sin)
+  constexpr int V = RopeIo<E>::V;
+  __shared__ int64_t s_pos[kRopeRows];
+  __shared__ int s_ok[kRopeRows];
+  const int tid = threadIdx.x, t0 = blockIdx.x * rows;
+  const int heads = a.H_q + a.H_kv, half = a.rot / 2;
+  const int turned = PAIRS ? a.rot / V : half / V, copied = a.rot / V;  // units; first copied piece
+  const int units = turned + a.d / V - copied;
+  const int all = min(rows, a.T - t0) * heads * units;
+  int u = tid % units, h = tid / units, r = h / heads;
+  h -= r * heads;
+  const int du = kRopeThreads % units, dh0 = kRopeThreads / units, dr = dh0 / heads,
+            dh = dh0 - dr * heads;
+  uint4 x4[kAhead], y4[kAhead];
+  uint4* out[kAhead];
+  int uu[kAhead], rr[kAhead];
+  auto load = [&](int e) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      uu[k] = -1;
+      if (e + k * kRopeThreads < all) {
+        const uint4* in = reinterpret_cast<const uint4*>(rope_in<E>(a, t0 + r, h));
+        out[k] = reinterpret_cast<uint4*>(rope_out<E>(a, t0 + r, h));
+        uu[k] = u;
+        rr[k] = r;
+        x4[k] = in[u < turned ? u : copied + (u - turned)];
+        if (!PAIRS && u < turned) y4[k] = in[u + turned];
+      }
+      u += du;
+      h += dh;
+      r += dr;
+      if (u >= units) u -= units, ++h;
+      if (h >= heads) h -= heads, ++r;
+    }
   };
-  auto row_out = [&](int r, int h) -> E* {
-    const int64_t t = t0 + r;
-    return h < a.H_q
-               ? static_cast<E*>(a.q_out) + t * a.q_out_stride + (int64_t)h * a.d
-               : static_cast<E*>(a.k_out) + t * a.k_out_stride + (int64_t)(h - a.H_q) * a.d;
-  };
-  if (a.interleaved ? a.rot % V == 0 : half % V == 0) {
-    // units: in the half layout a pair of pieces (p, p + half / V), else one piece; the
-    // pieces past rot are copied
-    const int turned = a.interleaved ? a.rot / V : half / V;
-    const int units = turned + (pieces - a.rot / V);
-    for (int e = tid; e < rows * heads * units; e += kRopeThreads) {
-      const int u = e % units, rh = e / units, h = rh % heads, r = rh / heads;
-      if (!s_ok[r]) continue;
-      const uint4* in = reinterpret_cast<const uint4*>(row_in(r, h));
-      uint4* out = reinterpret_cast<uint4*>(row_out(r, h));
-      if (u >= turned) {
-        const int p = a.rot / V + (u - turned);
-        if (in != out) out[p] = in[p];
+  load(tid);
+  rope_table(a, t0, rows, turn, s_pos, s_ok);
+  for (int e = tid;;) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (uu[k] < 0 || !s_ok[rr[k]]) continue;
+      if (uu[k] >= turned) {
+        out[k][copied + (uu[k] - turned)] = x4[k];
         continue;
       }
       float x[V], y[V];
-      const float2* cs = turn + r * half;
-      if (a.interleaved) {
-        RopeIo<E>::up(in[u], x);
+      const float2* cs = turn + rr[k] * half;
+      RopeIo<E>::up(x4[k], x);
+      if (PAIRS) {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          const float2 w = cs[u * (V / 2) + i];
+        for (int i = 0; i < V / 2; i += 2) {
+          const float4 w = *reinterpret_cast<const float4*>(cs + uu[k] * (V / 2) + i);
           y[2 * i] = x[2 * i] * w.x - x[2 * i + 1] * w.y;
           y[2 * i + 1] = x[2 * i] * w.y + x[2 * i + 1] * w.x;
+          y[2 * i + 2] = x[2 * i + 2] * w.z - x[2 * i + 3] * w.w;
+          y[2 * i + 3] = x[2 * i + 2] * w.w + x[2 * i + 3] * w.z;
         }
-        out[u] = RopeIo<E>::down(y);
+        out[k][uu[k]] = RopeIo<E>::down(y);
       } else {
         float z[V];
-        RopeIo<E>::up(in[u], x);
-        RopeIo<E>::up(in[u + turned], y);
+        RopeIo<E>::up(y4[k], y);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 w = cs[u * V + i];
+        for (int i = 0; i < V; i += 2) {
+          const float4 w = *reinterpret_cast<const float4*>(cs + uu[k] * V + i);
           z[i] = x[i] * w.x - y[i] * w.y;
           y[i] = x[i] * w.y + y[i] * w.x;
+          z[i + 1] = x[i + 1] * w.z - y[i + 1] * w.w;
+          y[i + 1] = x[i + 1] * w.w + y[i + 1] * w.z;
         }
-        out[u] = RopeIo<E>::down(z);
-        out[u + turned] = RopeIo<E>::down(y);
+        out[k][uu[k]] = RopeIo<E>::down(z);
+        out[k][uu[k] + turned] = RopeIo<E>::down(y);
       }
     }
-    return;
+    e += kAhead * kRopeThreads;
+    if (e >= all) break;
+    load(e);
   }
-  // any other width: one pair, or one copied element, per thread
+}
+
+// Any other width (rot not a whole number of pieces): one pair, or one copied element, per
+// thread and turn.
+template <typename E>
+__global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const RopeArgs a, int rows) {
+  extern __shared__ __align__(16) float2 turn[];
+  __shared__ int64_t s_pos[kRopeRows];
+  __shared__ int s_ok[kRopeRows];
+  const int tid = threadIdx.x, t0 = blockIdx.x * rows;
+  rope_table(a, t0, rows, turn, s_pos, s_ok);
+  const int heads = a.H_q + a.H_kv, half = a.rot / 2;
   const int units = half + (a.d - a.rot);
   for (int e = tid; e < rows * heads * units; e += kRopeThreads) {
     const int u = e % units, rh = e / units, h = rh % heads, r = rh / heads;
     if (!s_ok[r]) continue;
-    const E* in = row_in(r, h);
-    E* out = row_out(r, h);
+    const E* in = rope_in<E>(a, t0 + r, h);
+    E* out = rope_out<E>(a, t0 + r, h);
     if (u >= half) {
       out[a.rot + u - half] = in[a.rot + u - half];
       continue;
@@ -186,9 +240,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
 
 template <typename E>
 static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
-  const int rows = a.T >= 8 * device_sm_count() * 4 ? 8 : a.T >= 2 * device_sm_count() ? 2 : 1;
+  constexpr int V = RopeIo<E>::V;
+  const bool pairs = a.interleaved != 0;
+  const bool pieces = (pairs ? a.rot : a.rot / 2) % V == 0;
+  // about two rounds of loads per thread where there are rows enough to keep every SM busy
+  const int units = pieces ? (pairs ? a.rot / V : a.rot / 2 / V) + (a.d - a.rot) / V : a.d;
+  const int full = 2 * kAhead * kRopeThreads / ((a.H_q + a.H_kv) * units);
+  const int spread = a.T / (2 * device_sm_count());
+  const int most = full < spread ? full : spread;
+  const int rows = most < 1 ? 1 : most > kRopeRows ? kRopeRows : most;
   const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
-  rope_kernel<E><<<grid, kRopeThreads, (size_t)rows * (a.rot / 2) * sizeof(float2), s>>>(a, rows);
+  const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);
+  const auto kern = !pieces ? rope_any_kernel<E> : pairs ? rope_kernel<E, true> : rope_kernel<E, false>;
+  kern<<<grid, kRopeThreads, smem, s>>>(a, rows);
   return cudaGetLastError();
 }
 
