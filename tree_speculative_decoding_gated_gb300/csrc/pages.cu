@@ -160,65 +160,90 @@ __device__ __forceinline__ int rows_to_append(const AppendArgs& a, int b) {
   return n < 0 || n > a.path_len ? -1 : n;
 }
 
+// Groups of kAppendRows rows, numbered through the sequences in order (each by its own range:
+// ranges need not be sound or apart), a group per CTA and turn; blockIdx.y: the layer.
 __global__ void __launch_bounds__(128) pages_append_kernel(const AppendArgs a) {
   grid_dependency_wait();
   const tgdn_pages& p = a.p;
   __shared__ int64_t s_to[kAppendRows];  // page * page_size + position in the page, or -1
   __shared__ int s_row[kAppendRows];
-  const int layer = blockIdx.y, tid = threadIdx.x;
-  if (tid < kAppendRows) {
-    int b, i, row = -1;
-    if (a.path != nullptr) {
-      const int groups = (a.path_len + kAppendRows - 1) / kAppendRows;
-      b = blockIdx.x / groups;
-      i = (blockIdx.x % groups) * kAppendRows + tid;
-      const int n = rows_to_append(a, b);
-      if (i < n) {
-        const int node = a.path[(int64_t)b * a.path_len + i];
-        if (node >= 0 && node < a.cu[b + 1] - a.cu[b]) row = a.cu[b] + node;
-      }
-    } else {
-      const int t = blockIdx.x * kAppendRows + tid;
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
-      i = t - a.cu[b];
-      if (i >= 0 && i < rows_to_append(a, b)) row = t;
-    }
-    int64_t to = -1;
-    if (row >= 0) {
-      const int len = p.len[b], held = p.held[b];
-      const int64_t at = (int64_t)len + i;
-      if (sound(p, len, held) && at < (int64_t)held * p.page_size) {
-        const int page = p.table[(int64_t)b * p.max_pages + at / p.page_size];
-        if (page >= 0 && page < p.n_pages) to = (int64_t)page * p.page_size + at % p.page_size;
-      }
-    }
-    s_to[tid] = to;
-    s_row[tid] = row;
-  }
-  __syncthreads();
+  __shared__ int s_seq, s_first;         // sequence and first row of this group; -1: no more
+  const int layer = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int d8 = a.pool.d / 8, pieces = a.pool.H_kv * d8;
   const int64_t page8 = (int64_t)pieces * p.page_size;  // 16-byte pieces of a page
   uint4* kp = static_cast<uint4*>(a.pool.data) + (int64_t)layer * 2 * p.n_pages * page8;
   uint4* vp = kp + (int64_t)p.n_pages * page8;
   const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + layer * a.k_layer);
   const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + layer * a.v_layer);
-  for (int e = tid; e < kAppendRows * pieces; e += 128) {
-    const int r = e / pieces, c = e - r * pieces;
-    const int64_t to = s_to[r];
-    if (to < 0) continue;
-    const int h = c / d8, x = c - h * d8;
-    const int64_t page = to / p.page_size, in = to % p.page_size;
-    const int64_t dst = page * page8 + ((int64_t)h * p.page_size + in) * d8 + x;
-    const int64_t src = (int64_t)s_row[r];
-    const uint4 kv = ks[src * (a.k_row / 8) + c], vv = vs[src * (a.v_row / 8) + c];
-    kp[dst] = kv;
-    vp[dst] = vv;
+  int chunk = 0;       // (warp 0) sequences from here on ...
+  int64_t before = 0;  // ... begin at this group
+  for (int64_t x = blockIdx.x;; x += gridDim.x) {
+    if (tid < 32) {
+      int seq = -1, first = 0;
+      while (chunk < p.B) {
+        const int n = chunk + lane < p.B ? rows_to_append(a, chunk + lane) : 0;
+        const int groups = n > 0 ? (n + kAppendRows - 1) / kAppendRows : 0;
+        int64_t upto = groups;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+        if (x < before + total) {
+          const int f = __ffs(__ballot_sync(0xffffffffu, upto > x - before)) - 1;
+          seq = chunk + f;
+          first = (int)(x - before - __shfl_sync(0xffffffffu, upto - groups, f)) * kAppendRows;
+          break;
+        }
+        before += total;
+        chunk += 32;
+      }
+      if (lane == 0) {
+        s_seq = seq;
+        s_first = first;
+      }
+    }
+    __syncthreads();
+    const int b = s_seq;
+    if (b < 0) return;
+    if (tid < kAppendRows) {
+      const int i = s_first + tid, lo = a.cu[b];
+      int row = -1;
+      if (i < rows_to_append(a, b)) {
+        if (a.path == nullptr) {
+          row = lo + i;
+        } else {
+          const int node = a.path[(int64_t)b * a.path_len + i];
+          if (node >= 0 && node < a.cu[b + 1] - lo) row = lo + node;
+        }
+      }
+      int64_t to = -1;
+      if (row >= 0) {
+        const int len = p.len[b], held = p.held[b];
+        const int64_t at = (int64_t)len + i;
+        if (sound(p, len, held) && at < (int64_t)held * p.page_size) {
+          const int page = p.table[(int64_t)b * p.max_pages + at / p.page_size];
+          if (page >= 0 && page < p.n_pages) to = (int64_t)page * p.page_size + at % p.page_size;
+        }
+      }
+      s_to[tid] = to;
+      s_row[tid] = row;
+    }
+    __syncthreads();
+    for (int e = tid; e < kAppendRows * pieces; e += 128) {
+      const int r = e / pieces, c = e - r * pieces;
+      const int64_t to = s_to[r];
+      if (to < 0) continue;
+      const int h = c / d8, y = c - h * d8;
+      const int64_t page = to / p.page_size, in = to % p.page_size;
+      const int64_t dst = page * page8 + ((int64_t)h * p.page_size + in) * d8 + y;
+      const int64_t src = (int64_t)s_row[r];
+      const uint4 kv = ks[src * (a.k_row / 8) + c], vv = vs[src * (a.v_row / 8) + c];
+      kp[dst] = kv;
+      vp[dst] = vv;
+    }
+    __syncthreads();
   }
 }
 
@@ -259,13 +284,14 @@ __global__ void __launch_bounds__(128) pages_advance_kernel(const AppendArgs a, 
 }
 
 cudaError_t launch_pages_append(const AppendArgs& a, bool advance, cudaStream_t s) {
+  // groups there can be when the ranges are sound (each CTA goes on to further ones)
   const int64_t groups = a.path != nullptr
                              ? (int64_t)a.p.B * ((a.path_len + kAppendRows - 1) / kAppendRows)
-                             : ((int64_t)a.T + kAppendRows - 1) / kAppendRows;
-  if (groups > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (groups > 0) {
-    const cudaError_t e = launch_after(pages_append_kernel, dim3((unsigned)groups, a.pool.layers),
-                                       dim3(128), 0, s, a);
+                             : (int64_t)a.T / kAppendRows + a.p.B;
+  if (a.T > 0 && groups > 0) {
+    const int64_t most = 16 * device_sm_count();  // CTAs per layer that can be resident
+    const unsigned grid = (unsigned)(groups < most ? groups : most);
+    const cudaError_t e = launch_after(pages_append_kernel, dim3(grid, a.pool.layers), dim3(128), 0, s, a);
     if (e != cudaSuccess) return e;
   }
   return launch_after(pages_advance_kernel, dim3((a.p.B + 3) / 4), dim3(128), 0, s, a,

@@ -71,19 +71,27 @@ template <> struct RopeIo<__half> {
   }
 };
 
-// The sequence of row t, or -1: the last b with cu[b] <= t, if its range is sound.  Called
-// by a whole warp, which tests 32 offsets at a time.
+// The sequence of row t, or -1.  Called by a whole warp, which tests 32 offsets at a time:
+// the last b with cu[b] <= t, where its range is sound and holds t; offsets that decrease
+// somewhere can hide t's sequence from that, so otherwise the first sound range around t.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int T, int t) {
   const int lane = threadIdx.x & 31;
+  auto holds = [&](int b) {
+    const int c0 = cu[b], c1 = cu[b + 1];
+    return c0 >= 0 && c0 <= t && t < c1 && c1 <= T;
+  };
   int b = -1;
   for (int c = 0; c < B; c += 32) {
     const uint32_t below = __ballot_sync(0xffffffffu, c + lane < B && cu[c + lane] <= t);
     if (below) b = c + 31 - __clz(below);
     if (below != 0xffffffffu) break;
   }
-  if (b < 0) return -1;
-  const int c0 = cu[b], c1 = cu[b + 1];
-  return c0 >= 0 && t < c1 && c1 <= T ? b : -1;
+  if (b >= 0 && holds(b)) return b;
+  for (int c = 0; c < B; c += 32) {
+    const uint32_t in = __ballot_sync(0xffffffffu, c + lane < B && holds(min(c + lane, B - 1)));
+    if (in) return c + __ffs(in) - 1;
+  }
+  return -1;
 }
 
 // The rows' positions (a warp per row) and their cosines and sines, to shared memory.

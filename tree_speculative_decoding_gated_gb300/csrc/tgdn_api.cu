@@ -491,7 +491,7 @@ int tgdn_rope_freqs(int32_t rot, double theta, int32_t scaling, double factor,
       const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
       f = f / factor * r + f * (1.0 - r);
     }
-    freq[i] = static_cast<uint64_t>(std::ldexp(f / kTwoPi, 64));
+    freq[i] = static_cast<uint64_t>(std::rint(std::ldexp(f / kTwoPi, 64)));
   }
   *mscale = scaling == TGDN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
   return TGDN_OK;
