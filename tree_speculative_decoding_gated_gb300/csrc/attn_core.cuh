@@ -220,7 +220,9 @@ struct alignas(16) Bars {
   uint64_t sfull[2], pready[2][2], pvdone[2];
   uint64_t partfull[kFixRing], fixed[kFixRing];
   uint64_t maskfull[2], maskempty[2];
+  uint64_t stolen;
   uint64_t segfull[kRing], segempty[kRing];
+  uint4 steal;  // the answer to a request for another CTA's work
   Seg seg[kRing];
   int dirty[kRing], bad[kRing];
   uint32_t tmem;
@@ -302,6 +304,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     mbar_init(&br->qfull, 1);
     mbar_init(&br->qempty, 1);
     mbar_init(&br->drain, 1);
+    mbar_init(&br->stolen, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&br->sfull[i], 1);
       mbar_init(&br->pready[i][0], 4);
@@ -339,7 +342,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
 
   if (warp == kCopyWarp) {
     // ---------------- work list and copies
-    W work(a);
+    W work(a, &br->steal, &br->stolen);
     uint32_t cnt = 0, fix = 0;  // key and value tiles requested; values to be made safe
     int n_q = 0;       // items whose queries were requested
     auto slot_free = [&](uint32_t c) -> bool {
@@ -445,8 +448,10 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         page = next_page;
       }
     }
+    if (!ok && lane == 0) br->where = s.b;
+    while (work.finish(s))  // work that was taken over and will not be done
+      if (lane == 0) atomicCAS(&a.status[s.b], TGDN_SEQ_OK, TGDN_SEQ_TIMEOUT);
     if (!ok) {  // let the copies in flight land before the shared memory goes (bounded)
-      if (lane == 0) br->where = s.b;
       for (uint32_t c = cnt > NS ? cnt - NS : 0; c < cnt; ++c)
         (void)mbar_wait(&br->kvfull[c % NS], (c / NS) & 1);
       for (uint32_t c = fix > kFixRing ? fix - kFixRing : 0; c < fix; ++c)

@@ -80,7 +80,7 @@ struct PagedWork {
     upto = warp_sum_upto(tiles, lane);
     total = __shfl_sync(0xffffffffu, upto, 31);
   }
-  __device__ explicit PagedWork(const Args& args) : a(args), lane(threadIdx.x & 31) {
+  __device__ PagedWork(const Args& args, uint4*, uint64_t*) : a(args), lane(threadIdx.x & 31) {
     // (a call that ends early must leave nothing for the merge to read)
     if (a.part != nullptr && lane == 0) a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     load(0);
@@ -115,6 +115,7 @@ struct PagedWork {
     }
   }
 
+  __device__ bool finish(Seg&) { return false; }
   __device__ bool next(Seg& s) {
     while (x < x1) {
       for (;;) {

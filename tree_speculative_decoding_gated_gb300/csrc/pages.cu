@@ -94,6 +94,7 @@ __device__ __forceinline__ bool sound(const tgdn_pages& p, int len, int held) {
 // ----------------------------------------------------------------- reserve
 __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(tgdn_pages p, PagesWs w,
                                                                      const int32_t* add) {
+  grid_launch_dependents();
   grid_dependency_wait();
   // pages each sequence lacks and where they begin in the list of free pages
   int32_t *need = w.a, *off = w.b, *list = w.c;
@@ -163,6 +164,7 @@ __device__ __forceinline__ int rows_to_append(const AppendArgs& a, int b) {
 // Groups of kAppendRows rows, numbered through the sequences in order (each by its own range:
 // ranges need not be sound or apart), a group per CTA and turn; blockIdx.y: the layer.
 __global__ void __launch_bounds__(128) pages_append_kernel(const AppendArgs a) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const tgdn_pages& p = a.p;
   __shared__ int64_t s_to[kAppendRows];  // page * page_size + position in the page, or -1
@@ -249,6 +251,7 @@ __global__ void __launch_bounds__(128) pages_append_kernel(const AppendArgs a) {
 
 // Status of every sequence's append and, if asked for, its new length: a warp per sequence.
 __global__ void __launch_bounds__(128) pages_advance_kernel(const AppendArgs a, int advance) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const tgdn_pages& p = a.p;
   const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(tgdn_page
                                                                        int n, const int32_t* src,
                                                                        const int32_t* dst,
                                                                        int32_t* status) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < n; i += kPlanWarps) {
@@ -365,6 +369,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(tgdn_page
 // layer's keys or values of the last page.
 __global__ void __launch_bounds__(128) pages_fork_kernel(tgdn_pages p, tgdn_pool pool, PagesWs w,
                                                          const int32_t* src, const int32_t* dst) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const int i = blockIdx.x, tid = threadIdx.x;
   const int full = w.a[i], tail = w.b[i];
@@ -413,6 +418,7 @@ cudaError_t launch_pages_fork(const tgdn_pages& p, const tgdn_pool& pool, int n,
 
 // ----------------------------------------------------------------- free
 __global__ void __launch_bounds__(128) pages_free_kernel(tgdn_pages p, const int32_t* seq) {
+  grid_launch_dependents();
   grid_dependency_wait();
   __shared__ int s_held;
   const int b = seq[blockIdx.x], tid = threadIdx.x;
@@ -442,6 +448,7 @@ cudaError_t launch_pages_free(const tgdn_pages& p, int n, const int32_t* seq, cu
 // from n_live on goes (-1: it is free).
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(tgdn_pages p, PagesWs w,
                                                                           int32_t* n_live) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const int64_t all = 0x7fffffff;
   const int live = (int)list_pages<false>(p.refs, 0, p.n_pages, all, [](int64_t, int) {});
@@ -462,6 +469,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(tgdn_p
 constexpr int kMoveBytes = 16384;  // bytes per step of a CTA's copies
 
 __global__ void __launch_bounds__(256) pages_compact_kernel(tgdn_pages p, tgdn_pool pool, PagesWs w) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const int live = w.head[0], moves = w.head[1], tid = threadIdx.x;
   // tables: a warp per sequence; reference counts: a thread per move

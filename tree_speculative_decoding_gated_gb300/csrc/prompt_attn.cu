@@ -3,9 +3,11 @@
 //   o_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   within each sequence.
 //
 // The pipeline of attn_core.cuh over items (sequence, block of 2 x 128 query rows,
-// key/value head).  The kernel is persistent, one CTA per SM; items go out with each
-// sequence's last (longest) blocks first, the turns alternating in direction, so that the
-// CTAs' shares of the triangle even out without any count kept in memory.
+// key/value head).  One CTA per item is launched, each sequence's last (longest) blocks
+// first; the CTAs that run take over the places of those that have not started (cluster
+// launch control), so that a CTA's copies and first products of the next item go out while
+// it finishes the last and uneven lengths even out.  Against items dealt out in turns:
+// 16 prompts of up to 4001 tokens PLACE, 6 of up to 2500 PLACE.
 #include "attn_core.cuh"
 
 namespace tgdn {
@@ -13,11 +15,18 @@ namespace attn {
 
 struct PromptWork {
   const Args& a;
+  uint4* answer;
+  uint64_t* bar;
   int lane, chunk = 0;       // sequences from `chunk` on ...
   int before = 0;            // ... begin at this item
-  int turn = 0;
+  int asked = 0;             // requests made; the last one is open while open is set
+  bool open = false;
+  int64_t x;                 // the next item, or -1
 
-  __device__ explicit PromptWork(const Args& args) : a(args), lane(threadIdx.x & 31) {}
+  __device__ PromptWork(const Args& args, uint4* ans, uint64_t* b)
+      : a(args), answer(ans), bar(b), lane(threadIdx.x & 31), x(blockIdx.x) {
+    ask();
+  }
 
   static __device__ __forceinline__ bool valid(const Args& a, int lo, int hi) {
     return lo >= 0 && hi >= lo && hi <= a.T;
@@ -28,10 +37,44 @@ struct PromptWork {
       a.status[b] = valid(a, a.cu[b], a.cu[b + 1]) ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
   }
   static __device__ void last(const Args&, int) {}
-  __device__ bool next(Seg& s) {
-    const int grid = gridDim.x, c = blockIdx.x;
-    const int64_t x = (int64_t)turn * grid + ((turn & 1) ? grid - 1 - c : c);
-    ++turn;
+
+  // Requests the place of a CTA of this grid that has not started.
+  __device__ void ask() {
+    if (lane == 0) {
+      fence_proxy_async_smem();  // the last answer was read
+      mbar_arrive_expect_tx(bar, 16);
+      asm volatile(
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+          "[%1];" ::"r"(smem_addr(answer)),
+          "r"(smem_addr(bar))
+          : "memory");
+    }
+    __syncwarp();
+    ++asked;
+    open = true;
+  }
+  // The number of the CTA whose place was given, or -1 (none is left, or the answer did not
+  // come in time).
+  __device__ int64_t answered() {
+    const bool came = __all_sync(0xffffffffu, mbar_wait(bar, (asked - 1) & 1)) != 0;
+    open = false;
+    if (!came) return -1;
+    uint32_t got, cta;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(cta)
+        : "r"(smem_addr(answer))
+        : "memory");
+    __syncwarp();
+    return got ? (int64_t)cta : -1;
+  }
+  // Item x, if there is one (numbers mostly ascend: the search goes on where the last ended).
+  __device__ bool find(Seg& s) {
+    if (x < before) chunk = before = 0;
     const int blk = a.tpt * a.tiles;  // tokens per item
     for (; chunk < a.B; chunk += 32) {
       int lo = 0, N = 0;
@@ -69,6 +112,27 @@ struct PromptWork {
         return true;
       }
       before += total;
+    }
+    return false;
+  }
+  // The answer to the request made an item ago is there; the next one goes out at once.
+  __device__ bool next(Seg& s) {
+    while (x >= 0) {
+      const bool found = find(s);  // (numbers past the last item have no work)
+      x = answered();
+      if (x >= 0) ask();
+      if (found) return true;
+    }
+    return false;
+  }
+  // After an early end: the items taken over and not done, one at a time.  No request stays
+  // open when the shared memory goes.
+  __device__ bool finish(Seg& s) {
+    while (x >= 0 || open) {
+      if (x < 0) x = answered();
+      const bool found = x >= 0 && find(s);
+      x = -1;
+      if (found) return true;
     }
     return false;
   }
@@ -125,7 +189,7 @@ cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, f
   a.tiles = items(2) >= sms ? 2 : 1;
   const long n = items(a.tiles);
   if (n > 0x3fffffffL) return cudaErrorInvalidConfiguration;
-  const int grid = (int)(n < sms ? n : sms);
+  const int grid = (int)n;
   if (d > 64)
     return io == TGDN_BF16 ? launch<128, __nv_bfloat16>(a, q, k, v, grid, s)
                            : launch<128, __half>(a, q, k, v, grid, s);

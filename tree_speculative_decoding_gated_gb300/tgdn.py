@@ -569,7 +569,10 @@ def pages_workspace(pages: Pages) -> torch.Tensor:
 
 
 def _pages_ws(pages: Pages, ws) -> int:
-    return _dev(ws, torch.uint8, pages_workspace_bytes(pages), "ws")
+    d = pages.__dict__
+    if d["_struct"] is None or "_ws" not in d:
+        d["_ws"] = pages_workspace_bytes(pages)  # depends on the sizes alone
+    return _dev(ws, torch.uint8, d["_ws"], "ws")
 
 
 def pages_reserve(pages: Pages, add, ws, stream=None) -> None:
