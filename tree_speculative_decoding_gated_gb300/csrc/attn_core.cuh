@@ -58,6 +58,11 @@ struct Lay {
   static constexpr int kStages = DP == 64 ? 8 : PAGED ? 4 : 5;  // key and value tiles in flight
   static constexpr int kOffKV = 2 * kTile;              // (the two query tiles come first)
   static constexpr int kOffMisc = kOffKV + kStages * kTile;
+  // tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (DP each), and P over its own S, or
+  // apart where it fits
+  static constexpr bool kApart = DP == 64;
+  static constexpr uint32_t kColO = 256, kColP = kApart ? 256 + 2 * DP : 0;
+  static constexpr uint32_t kStepP = kApart ? 64 : 128;  // columns between P_0 and P_1
 };
 
 // One piece of work: key tiles [u0, u1) of an item.
@@ -474,8 +479,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       return __all_sync(0xffffffffu, wait_bar(bar, parity, abort)) != 0;
     };
     auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
-      // the previous O_t += P_t V has read P_t, which lies in S_t's columns
-      if (done[t] > 0 && !wait(&br->pvdone[t], (done[t] - 1) & 1)) return false;
+      // the previous O_t += P_t V has read P_t where that lies in S_t's columns
+      if (!L::kApart && done[t] > 0 && !wait(&br->pvdone[t], (done[t] - 1) & 1)) return false;
       tc_fence_after_sync();
       const uint32_t slot = c % NS;
       const uint32_t q = dQ + t * (L::kTile >> 4), k = dK + slot * (L::kTile >> 4);
@@ -487,18 +492,25 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       commit(&br->sfull[t]);
       return true;
     };
-    // O_t (+)= P_t V of the tile in slot c, 64 keys at a time as their P comes
-    auto pv = [&](int t, uint32_t c, bool first) -> bool {
+    // O_t (+)= P_t V of the tile in slot c, 64 keys at a time as their P comes.  With P apart
+    // the next S_t goes first (its columns were read before any P was written): the softmax
+    // warps then never wait for a product.
+    auto pv = [&](int t, uint32_t c, bool first, bool more) -> bool {
       const uint32_t slot = c % NS;
       const uint32_t v = dV + slot * (L::kTile >> 4);
       const uint32_t add = first ? 0u : 1u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!wait(&br->pready[t][h], done[t] & 1)) return false;
+        if (L::kApart && h == 0 && more) {
+          const uint32_t ck = c + 1;
+          if (!wait(&br->kvfull[ck % NS], (ck / NS) & 1) || !score(t, ck)) return false;
+        }
         tc_fence_after_sync();
 #pragma unroll
         for (int i = h * 4; i < h * 4 + 4; ++i)
-          mma_ts(utm + 256 + t * 128, utm + t * 128 + i * 8, v + i * 128, id_o, i > 0 ? 1u : add);
+          mma_ts(utm + L::kColO + t * DP, utm + L::kColP + t * L::kStepP + i * 8, v + i * 128, id_o,
+                 i > 0 ? 1u : add);
       }
       commit(&br->pvdone[t]);
       ++done[t];
@@ -531,12 +543,12 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           ok = wait(&br->fixed[fix % kFixRing], (fix / kFixRing) & 1);
           ++fix;
         }
-        if (ok && x0) ok = pv(0, cv, u == s.u0);
-        if (ok && y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
-        if (ok && x1) ok = pv(1, cv, u == s.u0);
+        if (ok && x0) ok = pv(0, cv, u == s.u0, y0);
+        if (!L::kApart && ok && y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
+        if (ok && x1) ok = pv(1, cv, u == s.u0, y1);
         if (!ok) break;
         commit(&br->kvempty[cv % NS]);
-        if (y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
+        if (!L::kApart && y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
         if (ok && u + 1 < s.u1) {
           commit(&br->kvempty[ck % NS]);
           if (u + 2 == s.u1) commit(&br->qempty);
@@ -639,7 +651,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + 256 + t * 128 + lanes;
+    const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + L::kColO + t * DP + lanes;
+    const uint32_t tP = tmem + L::kColP + t * L::kStepP + lanes;
     const float c2 = a.scale * 1.4426950408889634f;
     const float gap = kGap / a.scale;
     const int tok_in = row / a.G, g = row - tok_in * a.G;
@@ -699,13 +712,18 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
             for (int c = 2; c < 32; c += 2) mx[j] = max3(mx[j], x[j * 32 + c], x[j * 32 + c + 1]);
           }
           mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          if (L::kApart && done > 0) {  // the last product has read P and is in O
+            ok = wait_bar(&br->pvdone[t], (done - 1) & 1, abort);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after_sync();
+          }
           const bool need = live && mx[0] > m + gap;  // also the first finite maximum
           if (__any_sync(0xffffffffu, need)) {
             const float alpha =
                 need ? (m == -INFINITY ? 0.f : fast_exp2((m - mx[0]) * c2)) : 1.f;
             if (need) m = mx[0];
             la.x *= alpha, la.y *= alpha, lb.x *= alpha, lb.y *= alpha;
-            if (u > s.u0) {  // (the last product on O_t was done before S_t was issued)
+            if (u > s.u0) {  // (the last product on O_t is done)
 #pragma unroll 1
               for (int q = 0; q < DP / 16; ++q) {
                 float o[16];
@@ -732,7 +750,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
               else la = add2(la, y);
               w[c] = Elem<E>::pack(y.x, y.y);
             }
-            tmem_st16(tS + q * 16, w);
+            tmem_st16(tP + q * 16, w);
             if (q & 1) {  // 64 keys are ready
               tmem_st_wait();
               tc_fence_before_sync();
