@@ -42,7 +42,7 @@ namespace attn {
 constexpr int kKeys = 128;   // keys per tile
 constexpr int kRows = 128;   // query rows per row tile
 constexpr int kBlock = 384;
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kFixWarp = 10;
+constexpr int kMmaWarp = 8;  // (the first after the softmax warps)
 constexpr int kRing = 4;     // work items known ahead
 constexpr int kFixRing = 4;  // value tiles being made safe (at most 4 value tiles are in flight)
 constexpr float kGap = 8.f;  // lazy rescaling threshold (natural log units)
@@ -63,6 +63,11 @@ struct Lay {
   static constexpr bool kApart = DP == 64;
   static constexpr uint32_t kColO = 256, kColP = kApart ? 256 + 2 * DP : 0;
   static constexpr uint32_t kStepP = kApart ? 64 : 128;  // columns between P_0 and P_1
+  // warps: with P apart a product warp for each row tile (short products: one warp's own
+  // instructions would set the pace), else one for both, which keeps them half a step apart
+  static constexpr int kMmaWarps = kApart ? 2 : 1;
+  static constexpr int kCopyWarp = kMmaWarp + kMmaWarps, kFixWarp = kCopyWarp + 1;
+  static constexpr int kFixWarps = kBlock / 32 - kFixWarp;
 };
 
 // One piece of work: key tiles [u0, u1) of an item.
@@ -128,6 +133,21 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t fmt, int M, int N, int b_m
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// 32 columns of this thread's lane and their maximum (NaN values are passed over).
+__device__ __forceinline__ void ld_max32(uint32_t at, float* r, float& top) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+        "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+        "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]), "=f"(top)
+      : "r"(at)
+      : "memory");
+}
 // Until this thread's tensor-memory loads are complete; the operands keep every use of the
 // loaded registers behind the wait.
 __device__ __forceinline__ void ld_wait32(float* r) {
@@ -221,8 +241,8 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 
 struct alignas(16) Bars {
   uint64_t kvfull[8], kvempty[8];
-  uint64_t qfull, qempty, drain;
-  uint64_t sfull[2], pready[2][2], pvdone[2];
+  uint64_t qfull, qempty, drain[2];
+  uint64_t sfull[2], sread[2], pready[2][2], pvdone[2];
   uint64_t partfull[kFixRing], fixed[kFixRing];
   uint64_t maskfull[2], maskempty[2];
   uint64_t stolen;
@@ -304,36 +324,37 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&br->kvfull[i], 1);
-      mbar_init(&br->kvempty[i], 1);
+      mbar_init(&br->kvempty[i], L::kMmaWarps);
     }
     mbar_init(&br->qfull, 1);
-    mbar_init(&br->qempty, 1);
-    mbar_init(&br->drain, 1);
+    mbar_init(&br->qempty, L::kMmaWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&br->drain[i], 1);
     mbar_init(&br->stolen, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&br->sfull[i], 1);
+      mbar_init(&br->sread[i], 4);
       mbar_init(&br->pready[i][0], 4);
       mbar_init(&br->pready[i][1], 4);
       mbar_init(&br->pvdone[i], 1);
     }
     for (int i = 0; i < kFixRing; ++i) {
       mbar_init(&br->partfull[i], 1);
-      mbar_init(&br->fixed[i], 2);
+      mbar_init(&br->fixed[i], L::kFixWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&br->maskfull[i], 2);
+      mbar_init(&br->maskfull[i], L::kFixWarps);
       mbar_init(&br->maskempty[i], 8);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&br->segfull[i], 1);
-      mbar_init(&br->segempty[i], 1 + 8 + 2);
+      mbar_init(&br->segempty[i], L::kMmaWarps + 8 + L::kFixWarps);
     }
     fence_mbar_init();
     br->abort = 0;
     br->where = -1;
   }
   if (warp == kMmaWarp) tmem_alloc(&br->tmem, kTmemCols);
-  if (tid >= kCopyWarp * 32 && tid < kCopyWarp * 32 + (PAGED ? 5 : 3)) {
+  if (tid >= L::kCopyWarp * 32 && tid < L::kCopyWarp * 32 + (PAGED ? 5 : 3)) {
     const CUtensorMap* maps[5] = {qmap, kmap, vmap, kpmap, vpmap};
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[lane])) : "memory");
   }
@@ -345,7 +366,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
   volatile int* abort = &br->abort;
   bool ok = true;
 
-  if (warp == kCopyWarp) {
+  if (warp == L::kCopyWarp) {
     // ---------------- work list and copies
     W work(a, &br->steal, &br->stolen);
     uint32_t cnt = 0, fix = 0;  // key and value tiles requested; values to be made safe
@@ -463,8 +484,10 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         (void)mbar_wait(&br->partfull[c % kFixRing], (c / kFixRing) & 1);
       if (n_q > 0) (void)mbar_wait(&br->qfull, (n_q - 1) & 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp && warp < kMmaWarp + L::kMmaWarps) {
     // ---------------- products.  The whole warp runs this role with equal values.
+    constexpr bool kOwn = L::kMmaWarps == 2;  // this warp serves one row tile
+    const int mine = warp - kMmaWarp;
     uint32_t cnt = 0, fix = 0;    // tiles seen; value tiles made safe
     uint32_t done[2] = {0, 0};    // steps of each row tile
     constexpr uint32_t id_s = idesc(Elem<E>::kFmt, 128, kKeys, 0);
@@ -477,6 +500,11 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     const uint32_t dV = (smem_addr(smem + L::kOffKV) >> 4) | ((uint32_t)(L::kHalf >> 4) << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait_bar(bar, parity, abort)) != 0;
+    };
+    // An operand buffer is free once this warp's products that read it are done, or at once.
+    auto release = [&](uint64_t* bar, bool used) {
+      if (!kOwn || used) commit(bar);
+      else if (lane == 0) mbar_arrive(bar);
     };
     auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
       // the previous O_t += P_t V has read P_t where that lies in S_t's columns
@@ -493,19 +521,19 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       return true;
     };
     // O_t (+)= P_t V of the tile in slot c, 64 keys at a time as their P comes.  With P apart
-    // the next S_t goes first (its columns were read before any P was written): the softmax
-    // warps then never wait for a product.
+    // the next S_t goes out as soon as this one has been read, beside the softmax on it.
     auto pv = [&](int t, uint32_t c, bool first, bool more) -> bool {
       const uint32_t slot = c % NS;
       const uint32_t v = dV + slot * (L::kTile >> 4);
       const uint32_t add = first ? 0u : 1u;
+      if (L::kApart) {  // S_t is in the softmax threads' registers
+        if (!wait(&br->sread[t], done[t] & 1)) return false;
+        const uint32_t ck = c + 1;
+        if (more && (!wait(&br->kvfull[ck % NS], (ck / NS) & 1) || !score(t, ck))) return false;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!wait(&br->pready[t][h], done[t] & 1)) return false;
-        if (L::kApart && h == 0 && more) {
-          const uint32_t ck = c + 1;
-          if (!wait(&br->kvfull[ck % NS], (ck / NS) & 1) || !score(t, ck)) return false;
-        }
         tc_fence_after_sync();
 #pragma unroll
         for (int i = h * 4; i < h * 4 + 4; ++i)
@@ -525,17 +553,19 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       s.u0 = uniform(s.u0), s.u1 = uniform(s.u1), s.e0 = uniform(s.e0), s.e1 = uniform(s.e1);
       s.N = uniform(s.N), s.P = uniform(s.P), s.npre = uniform(s.npre), s.tok0 = uniform(s.tok0);
       ok = wait(&br->qfull, n & 1) && wait(&br->kvfull[cnt % NS], (cnt / NS) & 1);
-      const bool a0 = s.e0 > s.u0, a1 = s.e1 > s.u0;
-      if (ok && a0) ok = score(0, cnt);
-      if (ok && a1) ok = score(1, cnt);
+      // steps of the row tiles that this warp serves
+      const int e0 = kOwn && mine != 0 ? s.u0 : s.e0, e1 = kOwn && mine != 1 ? s.u0 : s.e1;
+      const int e = max(e0, e1);
+      if (ok && e0 > s.u0) ok = score(0, cnt);
+      if (ok && e1 > s.u0) ok = score(1, cnt);
       if (ok) {
-        commit(&br->kvempty[cnt % NS]);
-        if (s.u1 - s.u0 == 1) commit(&br->qempty);
+        release(&br->kvempty[cnt % NS], e > s.u0);
+        if (s.u1 - s.u0 == 1) release(&br->qempty, e > s.u0);
       }
       for (int u = s.u0; ok && u < s.u1; ++u) {
         const uint32_t cv = cnt + 1, ck = cnt + 2;  // this value tile, the next key tile
-        const bool x0 = u < s.e0, x1 = u < s.e1;    // steps of the row tiles
-        const bool y0 = u + 1 < s.e0, y1 = u + 1 < s.e1;
+        const bool x0 = u < e0, x1 = u < e1;
+        const bool y0 = u + 1 < e0, y1 = u + 1 < e1;
         ok = wait(&br->kvfull[cv % NS], (cv / NS) & 1);
         int lim;
         bool by_row;
@@ -547,11 +577,14 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         if (!L::kApart && ok && y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
         if (ok && x1) ok = pv(1, cv, u == s.u0, y1);
         if (!ok) break;
-        commit(&br->kvempty[cv % NS]);
-        if (!L::kApart && y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
-        if (ok && u + 1 < s.u1) {
-          commit(&br->kvempty[ck % NS]);
-          if (u + 2 == s.u1) commit(&br->qempty);
+        release(&br->kvempty[cv % NS], u < e);
+        if (u + 1 < s.u1) {
+          if (!L::kApart && y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
+          // (a tile this warp has no step for is awaited too, or its phases could be lapped)
+          if (kOwn && u + 1 >= e) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1);
+          if (!ok) break;
+          release(&br->kvempty[ck % NS], u + 1 < e);
+          if (u + 2 == s.u1) release(&br->qempty, u + 1 < e);
         }
         cnt += 2;
       }
@@ -563,13 +596,14 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       if (lane == 0) mbar_arrive(&br->segempty[r]);
     }
     // every product and every arrival it owes is done before the shared memory goes
-    commit(&br->drain);
-    (void)mbar_wait(&br->drain, 0);
+    commit(&br->drain[mine]);
+    (void)mbar_wait(&br->drain[mine], 0);
     __syncwarp();
-  } else if (warp >= kFixWarp) {
+  } else if (warp >= L::kFixWarp) {
     // ---------------- value rows that must not reach the product
-    const int ft = tid - kFixWarp * 32;  // 0 .. 63
-    W::first(a, ft);  // status words
+    constexpr int kFix = L::kFixWarps * 32;
+    const int ft = tid - L::kFixWarp * 32;  // 0 .. kFix - 1
+    W::first(a, ft, kFix);  // status words
     uint32_t cnt = 0, fix = 0;
     int built = 0;
     for (int n = 0; ok; ++n) {
@@ -584,11 +618,11 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         const int k = built++;
         if (k >= 2) ok = wait_bar(&br->maskempty[k & 1], ((k >> 1) - 1) & 1, abort);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        uint16_t* par = spar + (warp - kFixWarp) * kMaxNodes;
+        uint16_t* par = spar + (warp - L::kFixWarp) * kMaxNodes;
         __syncwarp();
         for (int i = lane; i < s.N; i += 32) par[i] = (uint16_t)a.parent[s.lo + i];
         __syncwarp();
-        for (int i = ft; i < 2 * a.tpt && s.tok0 + i < s.N; i += 64) {
+        for (int i = ft; i < 2 * a.tpt && s.tok0 + i < s.N; i += kFix) {
           uint64_t m[kMaxNodes / 64];
 #pragma unroll
           for (int w = 0; w < kMaxNodes / 64; ++w) m[w] = 0;
@@ -615,7 +649,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         uint4* tile = reinterpret_cast<uint4*>(smem + L::kOffKV + (cv % NS) * L::kTile);
         uint32_t acc = 0;
-        for (int i = ft; i < L::kTile / 16; i += 64) {
+        for (int i = ft; i < L::kTile / 16; i += kFix) {
           const int row = (i >> 3) & (kKeys - 1);
           if (row >= lim) {
             tile[i] = make_uint4(0, 0, 0, 0);
@@ -628,7 +662,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         if (acc & 0x80008000u) {  // a non-finite value among this thread's
           br->dirty[r] = 1;
           uint32_t* w32 = reinterpret_cast<uint32_t*>(tile);
-          for (int i = ft; i < L::kTile / 16; i += 64)
+          for (int i = ft; i < L::kTile / 16; i += kFix)
             for (int j = 0; j < 4; ++j) {
               uint32_t w = w32[i * 4 + j];
               const uint32_t top = ((w & Elem<E>::kExp) + Elem<E>::kStep) & 0x80008000u;
@@ -645,7 +679,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&br->segempty[r]);
     }
-    W::last(a, ft);  // outputs of sequences that have no work
+    W::last(a, ft, kFix);  // outputs of sequences that have no work
   } else {
     // ---------------- softmax: row tile t, one row per thread
     const int t = warp >> 2;
@@ -675,18 +709,26 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           ok = wait_bar(&br->sfull[t], done & 1, abort);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after_sync();
-          float x[kKeys];
+          float x[kKeys], mx[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, reinterpret_cast<float(&)[32]>(x[q * 32]));
+          for (int q = 0; q < 4; ++q) ld_max32(tS + q * 32, x + q * 32, mx[q]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) ld_wait32(x + q * 32);
-          // masks
+          asm volatile("" : "+f"(mx[0]), "+f"(mx[1]), "+f"(mx[2]), "+f"(mx[3]));  // (after the wait)
+          if (L::kApart) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&br->sread[t]);
+          }
+          // masks; the maxima again where they apply
+          bool masked = false;
           if constexpr (PAGED) {
             if (u >= s.npre) {
               if (u == max(s.u0, s.npre)) ok = wait_bar(&br->maskfull[built & 1], (built >> 1) & 1, abort);
               if (!(ok = __all_sync(0xffffffffu, ok))) break;
               const uint4 w4 = reinterpret_cast<const uint4*>(mask)[u - s.npre];
               const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+              masked = true;
 #pragma unroll
               for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -694,22 +736,25 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
                   if (!((w[q] >> c) & 1u)) x[q * 32 + c] = -INFINITY;
             } else if (s.P - u * kKeys < kKeys) {
               const int lim = s.P - u * kKeys;
+              masked = true;
 #pragma unroll
               for (int c = 0; c < kKeys; ++c)
                 if (c >= lim) x[c] = -INFINITY;
             }
           } else if (u * kKeys + kKeys - 1 > s.tok0) {
             const int lim = live ? tok - u * kKeys : -1;
+            masked = true;
 #pragma unroll
             for (int c = 0; c < kKeys; ++c)
               if (c > lim) x[c] = -INFINITY;
           }
-          float mx[4];  // four chains of three-input maxima
+          if (masked) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mx[j] = fmaxf(x[j * 32], x[j * 32 + 1]);
+            for (int j = 0; j < 4; ++j) {
+              mx[j] = fmaxf(x[j * 32], x[j * 32 + 1]);
 #pragma unroll
-            for (int c = 2; c < 32; c += 2) mx[j] = max3(mx[j], x[j * 32 + c], x[j * 32 + c + 1]);
+              for (int c = 2; c < 32; c += 2) mx[j] = max3(mx[j], x[j * 32 + c], x[j * 32 + c + 1]);
+            }
           }
           mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           if (L::kApart && done > 0) {  // the last product has read P and is in O

@@ -102,13 +102,13 @@ struct PagedWork {
   }
 
   // Sequences without work but with rows: zeros, and the word for a bad length.
-  static __device__ void first(const Args&, int) {}
-  static __device__ void last(const Args& a, int ft) {
+  static __device__ void first(const Args&, int, int) {}
+  static __device__ void last(const Args& a, int ft, int n) {
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       const Plan p = plan_of(a, b);
       if (p.nt || p.N <= 0 || p.st == TGDN_SEQ_BAD_RANGE || p.lo < 0 || p.lo + p.N > a.T) continue;
       const int v8 = a.H_q * a.d / 8;  // 16-byte pieces of a row
-      for (int64_t i = ft; i < (int64_t)p.N * v8; i += 64)
+      for (int64_t i = ft; i < (int64_t)p.N * v8; i += n)
         reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + (p.lo + i / v8) * a.o_stride)[i % v8] =
             make_uint4(0, 0, 0, 0);
       if (ft == 0) atomicCAS(&a.status[b], TGDN_SEQ_OK, TGDN_SEQ_BAD_PAGE);

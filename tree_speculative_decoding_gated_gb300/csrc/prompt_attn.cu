@@ -31,12 +31,12 @@ struct PromptWork {
   static __device__ __forceinline__ bool valid(const Args& a, int lo, int hi) {
     return lo >= 0 && hi >= lo && hi <= a.T;
   }
-  static __device__ void first(const Args& a, int ft) {
+  static __device__ void first(const Args& a, int ft, int n) {
     if (blockIdx.x != 0) return;
-    for (int b = ft; b < a.B; b += 64)
+    for (int b = ft; b < a.B; b += n)
       a.status[b] = valid(a, a.cu[b], a.cu[b + 1]) ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
   }
-  static __device__ void last(const Args&, int) {}
+  static __device__ void last(const Args&, int, int) {}
 
   // Requests the place of a CTA of this grid that has not started.
   __device__ void ask() {
