@@ -204,33 +204,43 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 // costs its 64 cycles also beside busy warps; under a branch or a predicate computed from the
 // lane number the same instructions took ~92.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024-byte stride, 128B swizzle
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
-                                       uint32_t add) {
+// D = A B over four k-steps of 16 elements (64 elements: one 128-byte half of both tiles), or
+// D += A B with add.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                        uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 u, v;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
       "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
+      "add.u32 u, %1, 2;\n\tadd.u32 v, %2, 2;\n\tmov.b64 x, {u, %5};\n\tmov.b64 y, {v, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.u32 u, %1, 4;\n\tadd.u32 v, %2, 4;\n\tmov.b64 x, {u, %5};\n\tmov.b64 y, {v, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.u32 u, %1, 6;\n\tadd.u32 v, %2, 6;\n\tmov.b64 x, {u, %5};\n\tmov.b64 y, {v, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(id), "r"(add), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
-                                       uint32_t add) {
+// The same over 64 keys with A (16-bit pairs, 8 columns per k-step) in tensor memory and B
+// MN-major (2048 bytes per k-step).
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                        uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 u, v;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
       "mov.b64 y, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t"
+      "add.u32 u, %1, 8;\n\tadd.u32 v, %2, 128;\n\tmov.b64 y, {v, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t"
+      "add.u32 u, %1, 16;\n\tadd.u32 v, %2, 256;\n\tmov.b64 y, {v, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t"
+      "add.u32 u, %1, 24;\n\tadd.u32 v, %2, 384;\n\tmov.b64 y, {v, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(id), "r"(add), "r"(kDescHi)
       : "memory");
 }
-// 32 bytes to a 32-byte boundary.
-__device__ __forceinline__ void st_global32(void* to, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-// Arrives on `bar` once every tensor-core instruction of that lane so far is complete.
+// Arrives on the barrier once every tensor-core instruction of that lane so far is complete.
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -239,6 +249,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global32(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 struct alignas(16) Bars {
   uint64_t kvfull[8], kvempty[8];
   uint64_t qfull, qempty, drain[2];
@@ -513,10 +529,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       const uint32_t slot = c % NS;
       const uint32_t q = dQ + t * (L::kTile >> 4), k = dK + slot * (L::kTile >> 4);
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i) {
-        const uint32_t at = ((i >> 2) * L::kHalf + (i & 3) * 32) >> 4;
-        mma_ss(utm + t * 128, q + at, k + at, id_s, i > 0);
-      }
+      for (int h = 0; h < L::kHalves; ++h)
+        mma_ss4(utm + t * 128, q + h * (L::kHalf >> 4), k + h * (L::kHalf >> 4), id_s, h);
       commit(&br->sfull[t]);
       return true;
     };
@@ -535,10 +549,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       for (int h = 0; h < 2; ++h) {
         if (!wait(&br->pready[t][h], done[t] & 1)) return false;
         tc_fence_after_sync();
-#pragma unroll
-        for (int i = h * 4; i < h * 4 + 4; ++i)
-          mma_ts(utm + L::kColO + t * DP, utm + L::kColP + t * L::kStepP + i * 8, v + i * 128, id_o,
-                 i > 0 ? 1u : add);
+        mma_ts4(utm + L::kColO + t * DP, utm + L::kColP + t * L::kStepP + h * 32, v + h * 512, id_o,
+                h | add);
       }
       commit(&br->pvdone[t]);
       ++done[t];
