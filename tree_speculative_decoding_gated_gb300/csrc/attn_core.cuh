@@ -172,6 +172,34 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   return mbar_try(bar, parity) || wait_slow(bar, parity, abort);
 }
 
+// The product warp's waits and arrivals take shared-memory addresses (its own instructions
+// set the pace of short steps).
+__device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+static __device__ __noinline__ bool wait_slow_at(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = global_ns();
+  while (!try_at(bar, parity)) {
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // Two-wide fp32 arithmetic and the three-input maximum (NaN operands are passed over).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -241,11 +269,10 @@ __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint
       : "memory");
 }
 // Arrives on the barrier once every tensor-core instruction of that lane so far is complete.
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_addr(bar))
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 
@@ -504,8 +531,29 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     // ---------------- products.  The whole warp runs this role with equal values.
     constexpr bool kOwn = L::kMmaWarps == 2;  // this warp serves one row tile
     const int mine = warp - kMmaWarp;
-    uint32_t cnt = 0, fix = 0;    // tiles seen; value tiles made safe
-    uint32_t done[2] = {0, 0};    // steps of each row tile
+    // Waits that fail are noted (`ok`) and looked at once per step: what is issued meanwhile
+    // stays within the operands' buffers and counts for nothing.
+    const uint32_t sb = smem_addr(br);
+    auto at = [&](const void* member) {
+      return sb + (uint32_t)(static_cast<const char*>(member) - reinterpret_cast<const char*>(br));
+    };
+    const uint32_t b_full = at(br->kvfull), b_empty = at(br->kvempty), b_fixed = at(br->fixed);
+    const uint32_t b_s = at(br->sfull), b_read = at(br->sread), b_p = at(br->pready),
+                   b_pv = at(br->pvdone), b_qempty = at(&br->qempty);
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (!try_at(bar, parity)) ok = wait_slow_at(bar, parity, abort) && ok;
+      __syncwarp();
+    };
+    // Place in the ring of key and value tiles.
+    struct Place {
+      uint32_t slot, parity;
+      __device__ void step() {
+        if (++slot == NS) slot = 0, parity ^= 1;
+      }
+    };
+    Place kp{0, 0}, vp{1, 0};   // the next key tile, the value tile of the step
+    uint32_t fix = 0;           // value tiles made safe
+    uint32_t done[2] = {0, 0};  // steps of each row tile
     constexpr uint32_t id_s = idesc(Elem<E>::kFmt, 128, kKeys, 0);
     constexpr uint32_t id_o = idesc(Elem<E>::kFmt, 128, DP, 1);
     const uint32_t utm = uniform(tmem);
@@ -514,92 +562,90 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     const uint32_t dQ = (smem_addr(smem) >> 4) | (1u << 16);
     const uint32_t dK = (smem_addr(smem + L::kOffKV) >> 4) | (1u << 16);
     const uint32_t dV = (smem_addr(smem + L::kOffKV) >> 4) | ((uint32_t)(L::kHalf >> 4) << 16);
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, wait_bar(bar, parity, abort)) != 0;
-    };
     // An operand buffer is free once this warp's products that read it are done, or at once.
-    auto release = [&](uint64_t* bar, bool used) {
+    auto release = [&](uint32_t bar, bool used) {
       if (!kOwn || used) commit(bar);
-      else if (lane == 0) mbar_arrive(bar);
+      else if (lane == 0) arrive_at(bar);
     };
-    auto score = [&](int t, uint32_t c) -> bool {  // S_t = Q_t K^T of the tile in slot c
+    auto score = [&](int t, uint32_t slot) {  // S_t = Q_t K^T of the tile in the slot
       // the previous O_t += P_t V has read P_t where that lies in S_t's columns
-      if (!L::kApart && done[t] > 0 && !wait(&br->pvdone[t], (done[t] - 1) & 1)) return false;
+      if (!L::kApart && done[t] > 0) wait(b_pv + t * 8, (done[t] - 1) & 1);
       tc_fence_after_sync();
-      const uint32_t slot = c % NS;
       const uint32_t q = dQ + t * (L::kTile >> 4), k = dK + slot * (L::kTile >> 4);
 #pragma unroll
       for (int h = 0; h < L::kHalves; ++h)
         mma_ss4(utm + t * 128, q + h * (L::kHalf >> 4), k + h * (L::kHalf >> 4), id_s, h);
-      commit(&br->sfull[t]);
-      return true;
+      commit(b_s + t * 8);
     };
-    // O_t (+)= P_t V of the tile in slot c, 64 keys at a time as their P comes.  With P apart
-    // the next S_t goes out as soon as this one has been read, beside the softmax on it.
-    auto pv = [&](int t, uint32_t c, bool first, bool more) -> bool {
-      const uint32_t slot = c % NS;
-      const uint32_t v = dV + slot * (L::kTile >> 4);
+    // O_t (+)= P_t V of the step, 64 keys at a time as their P comes.  With P apart the next
+    // S_t goes out as soon as this one has been read, beside the softmax on it.
+    auto pv = [&](int t, bool first, bool more) {
+      const uint32_t v = dV + vp.slot * (L::kTile >> 4);
       const uint32_t add = first ? 0u : 1u;
       if (L::kApart) {  // S_t is in the softmax threads' registers
-        if (!wait(&br->sread[t], done[t] & 1)) return false;
-        const uint32_t ck = c + 1;
-        if (more && (!wait(&br->kvfull[ck % NS], (ck / NS) & 1) || !score(t, ck))) return false;
+        wait(b_read + t * 8, done[t] & 1);
+        if (more) {
+          wait(b_full + kp.slot * 8, kp.parity);
+          score(t, kp.slot);
+        }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!wait(&br->pready[t][h], done[t] & 1)) return false;
+        wait(b_p + t * 16 + h * 8, done[t] & 1);
         tc_fence_after_sync();
         mma_ts4(utm + L::kColO + t * DP, utm + L::kColP + t * L::kStepP + h * 32, v + h * 512, id_o,
                 h | add);
       }
-      commit(&br->pvdone[t]);
+      commit(b_pv + t * 8);
       ++done[t];
-      return true;
     };
     for (int n = 0; ok; ++n) {
       const int r = n % kRing;
-      ok = wait(&br->segfull[r], (n / kRing) & 1);
-      if (!ok) break;
+      wait(at(&br->segfull[r]), (n / kRing) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       Seg s = br->seg[r];
       if (uniform(s.b) < 0) break;
       s.u0 = uniform(s.u0), s.u1 = uniform(s.u1), s.e0 = uniform(s.e0), s.e1 = uniform(s.e1);
       s.N = uniform(s.N), s.P = uniform(s.P), s.npre = uniform(s.npre), s.tok0 = uniform(s.tok0);
-      ok = wait(&br->qfull, n & 1) && wait(&br->kvfull[cnt % NS], (cnt / NS) & 1);
       // steps of the row tiles that this warp serves
       const int e0 = kOwn && mine != 0 ? s.u0 : s.e0, e1 = kOwn && mine != 1 ? s.u0 : s.e1;
       const int e = max(e0, e1);
-      if (ok && e0 > s.u0) ok = score(0, cnt);
-      if (ok && e1 > s.u0) ok = score(1, cnt);
-      if (ok) {
-        release(&br->kvempty[cnt % NS], e > s.u0);
-        if (s.u1 - s.u0 == 1) release(&br->qempty, e > s.u0);
-      }
-      for (int u = s.u0; ok && u < s.u1; ++u) {
-        const uint32_t cv = cnt + 1, ck = cnt + 2;  // this value tile, the next key tile
-        const bool x0 = u < e0, x1 = u < e1;
-        const bool y0 = u + 1 < e0, y1 = u + 1 < e1;
-        ok = wait(&br->kvfull[cv % NS], (cv / NS) & 1);
+      wait(at(&br->qfull), n & 1);
+      wait(b_full + kp.slot * 8, kp.parity);
+      if (e0 > s.u0) score(0, kp.slot);
+      if (e1 > s.u0) score(1, kp.slot);
+      release(b_empty + kp.slot * 8, e > s.u0);
+      if (s.u1 - s.u0 == 1) release(b_qempty, e > s.u0);
+      kp.step(), kp.step();
+      for (int u = s.u0; u < s.u1; ++u) {
+        const bool x0 = u < e0, x1 = u < e1;          // this warp's steps
+        const bool y0 = u + 1 < e0, y1 = u + 1 < e1;  // and next scores
+        wait(b_full + vp.slot * 8, vp.parity);
         int lim;
         bool by_row;
-        if (ok && tile_part<PAGED>(s, u, lim, by_row)) {
-          ok = wait(&br->fixed[fix % kFixRing], (fix / kFixRing) & 1);
+        if (tile_part<PAGED>(s, u, lim, by_row)) {
+          wait(b_fixed + (fix % kFixRing) * 8, (fix / kFixRing) & 1);
           ++fix;
         }
-        if (ok && x0) ok = pv(0, cv, u == s.u0, y0);
-        if (!L::kApart && ok && y0) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(0, ck);
-        if (ok && x1) ok = pv(1, cv, u == s.u0, y1);
-        if (!ok) break;
-        release(&br->kvempty[cv % NS], u < e);
-        if (u + 1 < s.u1) {
-          if (!L::kApart && y1) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1) && score(1, ck);
-          // (a tile this warp has no step for is awaited too, or its phases could be lapped)
-          if (kOwn && u + 1 >= e) ok = wait(&br->kvfull[ck % NS], (ck / NS) & 1);
-          if (!ok) break;
-          release(&br->kvempty[ck % NS], u + 1 < e);
-          if (u + 2 == s.u1) release(&br->qempty, u + 1 < e);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (x0) pv(0, u == s.u0, y0);
+        if (!L::kApart && y0) {
+          wait(b_full + kp.slot * 8, kp.parity);
+          score(0, kp.slot);
         }
-        cnt += 2;
+        if (x1) pv(1, u == s.u0, y1);
+        release(b_empty + vp.slot * 8, u < e);
+        if (u + 1 < s.u1) {
+          // (a tile this warp has no step for is awaited too, or its phases could be lapped)
+          if ((!L::kApart && !y0) || (kOwn && u + 1 >= e)) wait(b_full + kp.slot * 8, kp.parity);
+          if (!L::kApart && y1) score(1, kp.slot);
+          release(b_empty + kp.slot * 8, u + 1 < e);
+          if (u + 2 == s.u1) release(b_qempty, u + 1 < e);
+          kp.step(), kp.step();
+        }
+        vp.step(), vp.step();
       }
+      ok = __all_sync(0xffffffffu, ok) != 0;
       if (!ok) {
         if (lane == 0) br->where = s.b;
         break;
@@ -608,7 +654,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       if (lane == 0) mbar_arrive(&br->segempty[r]);
     }
     // every product and every arrival it owes is done before the shared memory goes
-    commit(&br->drain[mine]);
+    commit(at(&br->drain[mine]));
     (void)mbar_wait(&br->drain[mine], 0);
     __syncwarp();
   } else if (warp >= L::kFixWarp) {
