@@ -19,7 +19,7 @@ namespace attn {
 
 constexpr int kMinShare = 4;  // key tiles per CTA below which a cut costs more than it saves
 constexpr int kSplitTiles = 6;  // caches that can hold no more key tiles than this are never cut
-constexpr int kItemCost = 1;  // an item's start and output, in key tiles
+constexpr int kItemCost = 2;  // an item's start and output, in key tiles
 
 // Cached and tree key tiles of sequence b; 0: no work (empty, or an error).
 struct Plan {
@@ -179,7 +179,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   pipeline<DP, E, true, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
 }
 
-// Joins the parts of the item that begins in CTA blockIdx.x's run and goes on into later
+// Joins the parts of the item that begins in CTA blockIdx.y's run and goes on into later
 // ones, 32 query rows per CTA: a thread holds four columns (or a few times four) of one row.
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
 constexpr int kMergeRows = 32;
@@ -187,10 +187,10 @@ template <int DP, typename E>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ Args a) {
   __shared__ __align__(16) uint8_t s_out[kMergeRows][DP * 2 + 16];
   grid_dependency_wait();
-  const int c = blockIdx.x, tid = threadIdx.x;
+  const int c = blockIdx.y, tid = threadIdx.x;  // (an item's row groups go to different SMs)
   const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
   if (d0.x < 0) return;
-  const int r0 = blockIdx.y * kMergeRows, R = min(kMergeRows, a.part_rows - r0);
+  const int r0 = blockIdx.x * kMergeRows, R = min(kMergeRows, a.part_rows - r0);
   if ((r0 / kRows) * a.tpt + d0.w >= d0.z) return;  // no row of this row tile exists
   int rp = 1;  // threads side by side over rows: the power of two from R up
   while (rp < R) rp *= 2;
@@ -275,7 +275,7 @@ static cudaError_t launch(const Args& a, int grid, const CUtensorMap& q, const C
   if (e != cudaSuccess) return e;
   e = launch_after(kern, dim3(grid), dim3(kBlock), smem, s, q, k, v, kp, vp, a);
   if (e != cudaSuccess || a.part == nullptr) return e;
-  return launch_after(paged_merge_kernel<DP, E>, dim3(grid, (a.part_rows + kMergeRows - 1) / kMergeRows), dim3(256), 0, s,
+  return launch_after(paged_merge_kernel<DP, E>, dim3((a.part_rows + kMergeRows - 1) / kMergeRows, grid), dim3(256), 0, s,
                       a);
 }
 
