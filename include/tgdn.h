@@ -403,13 +403,14 @@ int tgdn_rope(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d, int32_
  * (cu[b] <= t < cu[b+1]) attends to rows cu[b] .. t,
  *   o[t][h] = softmax_j(scale * q[t][h] . k_j) v_j,
  * query head h reading key/value head h / (H_q / H_kv).
- *   cu     [B + 1] int32 (device); a sequence whose range leaves [0, T) is skipped
+ *   cu     [B + 1] int32 (device), non-decreasing; a sequence whose range leaves [0, T) or
+ *          begins before the end of an earlier one is skipped (its rows are not written)
  *   q, o   [T][H_q][d], k, v [T][H_kv][d] of io dtype (bf16 or f16); o overlaps no input
  *   status [B] int32, written: TGDN_SEQ_OK, _BAD_RANGE or _TIMEOUT
  *   ws     tgdn_prompt_attention_workspace_bytes() bytes (may be NULL when that is 0)
  * A value that only masked positions hold, NaN and infinities included, reaches no row.
- * d a multiple of 8, 8 .. 128; H_q / H_kv a whole number, at most 128; strides multiples
- * of 8 elements and at least heads * d; pointers 16-byte aligned; scale positive and
+ * T at most 2^30; d a multiple of 8, 8 .. 128; H_q / H_kv a whole number, at most 128;
+ * strides multiples of 8 elements and at least heads * d; pointers 16-byte aligned; scale positive and
  * finite.  Scores, softmax statistics and sums are fp32; the probabilities enter the
  * second product rounded to the io type.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG,
  * TGDN_EUNSUPPORTED or TGDN_ECUDA. */
@@ -471,9 +472,9 @@ int tgdn_pages_reserve(const tgdn_pages* pages, const int32_t* add, void* ws,
  *         H_kv * d), `layer` elements between layers (a multiple of 8)
  * With advance != 0 len[b] then grows by the rows written; without it the lengths stay
  * (layers appended one by one, the last call advancing).  A sequence whose rows leave
- * [cu[b], cu[b+1]) or [0, T), or do not fit its pages, is not written
- * (TGDN_SEQ_BAD_RANGE, TGDN_SEQ_NO_PAGES or TGDN_SEQ_BAD_PAGE).  path_len is path's
- * second dimension.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
+ * [cu[b], cu[b+1]) or [0, T), or do not fit its pages, is not advanced
+ * (TGDN_SEQ_BAD_RANGE, TGDN_SEQ_NO_PAGES or TGDN_SEQ_BAD_PAGE); its own pages may then
+ * hold some of the rows past len[b].  path_len is path's second dimension.  Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
 int tgdn_pages_append(const tgdn_pages* pages, const tgdn_pool* pool, int32_t T,
                       const int32_t* cu, const int32_t* path, int32_t path_len,
                       const int32_t* n_path, const void* k, int64_t k_layer, int64_t k_row,

@@ -145,6 +145,24 @@ def test_bad_ranges_are_skipped():
     assert bool(torch.isnan(o[50:]).all())
 
 
+def test_overlapping_ranges_are_skipped():
+    """More rows claimed than there are: the later claims are refused, nothing else is lost."""
+    T = 700
+    cu, q, k, v = make([T], 2, 1, 64, BF, seed=14)
+    ranges = [0, 300, 100, 450, 0, T] + [0, T] * 40 + [T]
+    cu2 = torch.tensor(ranges, dtype=torch.int32, device="cuda")
+    o, st = run(cu2, q, k, v, 0.1)
+    want, high = [], 0
+    for lo, hi in zip(ranges[:-1], ranges[1:]):
+        sound = lo <= hi
+        want.append(0 if sound and lo >= high else 7)
+        high = max(high, hi) if sound else high
+    assert st.tolist() == want and want[0] == 0 and want[2] == 7 and want[-1] == 0
+    ref, tol = attend(q[:300], k[:300], v[:300], np.tril(np.ones((300, 300), bool)), 0.1)
+    assert_within(o[:300], ref, tol)
+    assert bool(torch.isnan(o[300:]).all())
+
+
 def test_no_rows():
     cu = torch.zeros(4, dtype=torch.int32, device="cuda")
     e = torch.empty((0, 2, 64), dtype=BF, device="cuda")

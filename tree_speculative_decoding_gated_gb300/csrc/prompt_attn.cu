@@ -6,8 +6,9 @@
 // key/value head).  One CTA per item is launched, each sequence's last (longest) blocks
 // first; the CTAs that run take over the places of those that have not started (cluster
 // launch control), so that a CTA's copies and first products of the next item go out while
-// it finishes the last and uneven lengths even out.  Against items dealt out in turns:
-// 16 prompts of up to 4001 tokens PLACE, 6 of up to 2500 PLACE.
+// it finishes the last and uneven lengths even out.  Against items dealt out in turns,
+// 16 prompts of up to 4001 tokens (d = 128): 168 us after 192; items of one length lose a
+// little by the requests (6 prompts of up to 2500 tokens, d = 64: 49.5 us after 46.5).
 #include "attn_core.cuh"
 
 namespace tgdn {
@@ -19,6 +20,7 @@ struct PromptWork {
   uint64_t* bar;
   int lane, chunk = 0;       // sequences from `chunk` on ...
   int before = 0;            // ... begin at this item
+  int high = 0;              // ... and may use rows from this one on
   int asked = 0;             // requests made; the last one is open while open is set
   bool open = false;
   int64_t x;                 // the next item, or -1
@@ -28,13 +30,40 @@ struct PromptWork {
     ask();
   }
 
-  static __device__ __forceinline__ bool valid(const Args& a, int lo, int hi) {
-    return lo >= 0 && hi >= lo && hi <= a.T;
+  // The rows of this lane's sequence c + lane (whole warp): false when its range leaves [0, T)
+  // or begins below an earlier one's end (`high`: the end of those before c), so that no row
+  // has two sequences and the rows bound the items.
+  static __device__ bool range_of(const Args& a, int c, int high, int lane, int& lo, int& N,
+                                  int& next_high) {
+    lo = N = 0;
+    int hi = 0;
+    bool good = c + lane < a.B;
+    if (good) {
+      lo = a.cu[c + lane];
+      hi = a.cu[c + lane + 1];
+      good = lo >= 0 && hi >= lo && hi <= a.T;
+    }
+    int top = good ? hi : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, top, o);
+      if (lane >= o) top = max(top, y);
+    }
+    int under = __shfl_up_sync(0xffffffffu, top, 1);
+    under = lane == 0 ? high : max(under, high);
+    next_high = max(high, __shfl_sync(0xffffffffu, top, 31));
+    good = good && lo >= under;
+    N = good ? hi - lo : 0;
+    return good;
   }
-  static __device__ void first(const Args& a, int ft, int n) {
-    if (blockIdx.x != 0) return;
-    for (int b = ft; b < a.B; b += n)
-      a.status[b] = valid(a, a.cu[b], a.cu[b + 1]) ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
+  static __device__ void first(const Args& a, int ft, int) {
+    if (blockIdx.x != 0 || ft >= 32) return;
+    int high = 0;
+    for (int c = 0; c < a.B; c += 32) {
+      int lo, N;
+      const bool good = range_of(a, c, high, ft, lo, N, high);
+      if (c + ft < a.B) a.status[c + ft] = good ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
+    }
   }
   static __device__ void last(const Args&, int, int) {}
 
@@ -74,15 +103,11 @@ struct PromptWork {
   }
   // Item x, if there is one (numbers mostly ascend: the search goes on where the last ended).
   __device__ bool find(Seg& s) {
-    if (x < before) chunk = before = 0;
+    if (x < before) chunk = before = high = 0;
     const int blk = a.tpt * a.tiles;  // tokens per item
     for (; chunk < a.B; chunk += 32) {
-      int lo = 0, N = 0;
-      if (chunk + lane < a.B) {
-        lo = a.cu[chunk + lane];
-        const int hi = a.cu[chunk + lane + 1];
-        N = valid(a, lo, hi) ? hi - lo : 0;
-      }
+      int lo, N, next_high;
+      (void)range_of(a, chunk, high, lane, lo, N, next_high);
       const int items = (N + blk - 1) / blk * a.H_kv;
       int upto = items;
 #pragma unroll
@@ -91,7 +116,7 @@ struct PromptWork {
         if (lane >= o) upto += y;
       }
       const int total = __shfl_sync(0xffffffffu, upto, 31);
-      if (x < (int64_t)before + total) {
+      if (x < before + total) {
         const int at = (int)(x - before);
         const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
         s.b = chunk + f;
@@ -112,6 +137,7 @@ struct PromptWork {
         return true;
       }
       before += total;
+      high = next_high;
     }
     return false;
   }

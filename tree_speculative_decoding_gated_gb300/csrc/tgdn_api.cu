@@ -538,6 +538,7 @@ int tgdn_prompt_attention(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32
   if (B < 0 || T < 0) return TGDN_EINVAL;
   const int rc = check_attn(H_q, H_kv, d, io, scale);
   if (rc != TGDN_OK) return rc;
+  if (T > (1 << 30)) return TGDN_ETOOBIG;
   if (B == 0) return TGDN_OK;
   if (!cu || !status) return TGDN_EINVAL;
   if (T > 0) {
