@@ -72,6 +72,44 @@ def test_many_items_per_cta():
     check(lens, q, k, v, 0.088, o)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("H_q,H_kv,d", [(1, 1, 128), (8, 1, 64), (4, 4, 96), (2, 1, 40)])
+@pytest.mark.parametrize("lens", [[768], [1024], [1100, 900], [769, 1, 2000], [1537, 1000, 0]])
+def test_few_long_prompts(lens, H_q, H_kv, d, dtype):
+    """One row tile per item, key tiles in turn to both pipelines (even and odd counts, items of
+    one and two key tiles next to long ones)."""
+    cu, q, k, v = make(lens, H_q, H_kv, d, dtype, seed=sum(lens) + d, fused=d == 96)
+    o, st = run(cu, q, k, v, d ** -0.5)
+    assert st.tolist() == [0] * len(lens)
+    check(lens, q, k, v, d ** -0.5, o)
+    again, _ = run(cu, q, k, v, d ** -0.5)
+    assert torch.equal(o, again)
+
+
+@pytest.mark.parametrize("at", [0, 130, 700, 899])
+def test_one_pipeline_holds_all_the_weight(at):
+    """A key that outweighs every other one, in either pipeline's tiles; rows before it see none
+    of it."""
+    cu, q, k, v = make([900], 2, 1, 128, HF, seed=21)
+    q[:] = 0.5
+    k[:] = 0.25 * torch.sign(k)
+    k[at] = 4.0
+    o, _ = run(cu, q, k, v, 0.3)
+    check([900], q, k, v, 0.3, o)
+
+
+def test_non_finite_values_in_either_pipeline():
+    cu, q, k, v = make([1000], 2, 1, 64, BF, seed=22)
+    v[333, 0, 5] = float("nan")
+    v[600, 0, 9] = float("inf")
+    o, _ = run(cu, q, k, v, 0.1)
+    assert bool(torch.isfinite(o[:333]).all())
+    assert bool(torch.isnan(o[333:, :, 5]).all()) and bool(torch.isfinite(o[:600, :, 9]).all())
+    assert bool((o[600:, :, 9] == float("inf")).all())
+    keep = [c for c in range(64) if c not in (5, 9)]
+    assert bool(torch.isfinite(o[:, :, keep]).all())
+
+
 @pytest.mark.parametrize("gain,scale", [(30.0, 0.088), (0.0, 1.0), (2.0, 1e-4), (200.0, 0.3)])
 def test_peaked_and_flat_softmax(gain, scale):
     """Large logits (the running maximum moves over many tiles) and flat ones.  The tolerance

@@ -12,6 +12,8 @@
 // cut ones; the parts of a cut item (O unnormalised, reference maximum, sum) go to the
 // workspace and paged_merge_kernel joins them in order of their keys, so results do not
 // depend on timing.  Without a workspace items stay whole.
+#include <algorithm>
+
 #include "attn_core.cuh"
 
 namespace tgdn {
@@ -150,6 +152,7 @@ struct PagedWork {
         s.part = s.u0 == 0 && s.u1 == nt ? -1 : (n == 0 ? 0 : 1);
         s.e0 = s.u1;
         s.e1 = s.tok0 + a.tpt < s.N ? s.u1 : 0;
+        s.alt = 0;
         if (s.u0 == 0 && s.u1 < nt) {
           d0 = make_int4(s.b, s.lo, s.N, s.tok0);
           d1 = make_int4(s.hk, (int)divide(x_item + nt - 1, share), s.part, 0);
@@ -176,15 +179,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   extern __shared__ uint8_t pg_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(pg_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  pipeline<DP, E, true, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
+  pipeline<DP, E, true, false, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.y's run and goes on into later
-// ones, 32 query rows per CTA: a thread holds four columns (or a few times four) of one row.
+// ones, 32 query rows per CTA:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
+// First the weights, a lane per part, so that all statistics are under way at once; then
+// the sums, a thread per row and four columns, whose loads wait for nothing.  What few rows
+// leave of the CTA takes parts in turn.
 constexpr int kMergeRows = 32;
+constexpr int kMaxParts = 160;
 template <int DP, typename E>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ Args a) {
+  __shared__ float s_w[kMaxParts][kMergeRows];
+  __shared__ float s_inv[kMergeRows];
+  __shared__ float4 s_sum[256];
   __shared__ __align__(16) uint8_t s_out[kMergeRows][DP * 2 + 16];
   grid_dependency_wait();
   const int c = blockIdx.y, tid = threadIdx.x;  // (an item's row groups go to different SMs)
@@ -192,42 +202,88 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   if (d0.x < 0) return;
   const int r0 = blockIdx.x * kMergeRows, R = min(kMergeRows, a.part_rows - r0);
   if ((r0 / kRows) * a.tpt + d0.w >= d0.z) return;  // no row of this row tile exists
+  // part i lies in CTA c + i's first slot, the first part in the slot its CTA named
+  const int parts = min(d1.y - c + 1, kMaxParts);
+  auto slot = [&](int i) -> int64_t { return 2 * (c + i) + (i == 0 ? d1.z : 0); };
   int rp = 1;  // threads side by side over rows: the power of two from R up
   while (rp < R) rp *= 2;
-  const int r = tid & (rp - 1), cg0 = tid / rp, step = 256 / rp;
-  constexpr int C = DP / 4, kPer = C / 8;  // column groups; the most of one thread
-  float M = -INFINITY, sum = 0.f;
-  float4 acc[kPer];
+  constexpr int C = DP / 4, kPer = C / 8;      // column groups; the most of one thread
+  constexpr int kNext = 4;                     // parts under way
+  const int r = tid & (rp - 1), over = tid / rp;
+  const int step = min(256 / rp, C);           // threads over the columns
+  const int turns = 256 / rp / step;           // and over the parts
+  const int cg0 = over % step, turn = over / step;
+  const float4* part = reinterpret_cast<const float4*>(a.part) + r0 + min(r, R - 1);
+  float4 acc[kPer], o[kNext][kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // part i lies in CTA i's first slot, the first part in the slot its CTA named
-  auto slot = [&](int i) -> int64_t { return 2 * i + (i == c ? d1.z : 0); };
-  if (r < R && cg0 < C) {
-    const float2* ml = a.part_ml + r0 + r;
-    const float4* part = reinterpret_cast<const float4*>(a.part) + r0 + r;
-#pragma unroll 4
-    for (int i = c; i <= d1.y; ++i) {
-      const float2 v = ml[slot(i) * a.part_rows];
-      if (v.y != 0.f) M = fmaxf(M, v.x);
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kNext; ++j)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (i0 + j * turns < parts && cg0 + k * step < C)
+          o[j][k] = part[(slot(i0 + j * turns) * C + cg0 + k * step) * a.part_rows];
+  };
+  load(turn);  // (needs no weights)
+  {
+    const int sub = min(32, 256 / rp), rw = tid / sub, i0 = tid % sub;  // sub lanes per row
+    const float2* ml = a.part_ml + r0 + min(rw, R - 1);
+    float2 v[kNext];  // (all there are, but for many parts of many rows)
+    float M = -INFINITY, sum = 0.f;
+    for (int b = i0; b < parts; b += kNext * sub) {
+#pragma unroll
+      for (int j = 0; j < kNext; ++j) {
+        const int i = b + j * sub;
+        v[j] = i < parts ? ml[slot(i) * a.part_rows] : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < kNext; ++j)
+        if (v[j].y != 0.f) M = fmaxf(M, v[j].x);
     }
-#pragma unroll 4
-    for (int i = c; i <= d1.y; ++i) {
-      const float2 v = ml[slot(i) * a.part_rows];
-      const float w = v.y == 0.f ? 0.f : fast_exp2(v.x - M);
-      sum = fmaf(w, v.y, sum);
+    for (int o = sub / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int b = i0; b < parts; b += kNext * sub) {
+#pragma unroll
+      for (int j = 0; j < kNext; ++j) {
+        const int i = b + j * sub;
+        if (i >= parts) continue;
+        if (parts > kNext * sub) v[j] = ml[slot(i) * a.part_rows];
+        const float w = v[j].y == 0.f ? 0.f : fast_exp2(v[j].x - M);
+        sum = fmaf(w, v[j].y, sum);
+        if (rw < R) s_w[i][rw] = w;
+      }
+    }
+    for (int o = sub / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (rw < R && i0 == 0) s_inv[rw] = sum == 0.f ? 0.f : 1.f / sum;
+  }
+  __syncthreads();
+  for (int i0 = turn; i0 < parts; i0 += kNext * turns) {
+    if (i0 != turn) load(i0);
+#pragma unroll
+    for (int j = 0; j < kNext; ++j) {
+      const int i = i0 + j * turns;
+      const float w = i < parts && r < R ? s_w[i][r] : 0.f;
+      if (w == 0.f) continue;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (cg0 + k * step >= C) continue;
-        const float4 o = part[(slot(i) * C + cg0 + k * step) * a.part_rows];
-        if (w != 0.f) {
-          acc[k].x = fmaf(w, o.x, acc[k].x);
-          acc[k].y = fmaf(w, o.y, acc[k].y);
-          acc[k].z = fmaf(w, o.z, acc[k].z);
-          acc[k].w = fmaf(w, o.w, acc[k].w);
-        }
+        acc[k].x = fmaf(w, o[j][k].x, acc[k].x);
+        acc[k].y = fmaf(w, o[j][k].y, acc[k].y);
+        acc[k].z = fmaf(w, o[j][k].z, acc[k].z);
+        acc[k].w = fmaf(w, o[j][k].w, acc[k].w);
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  }
+  if (turns > 1) {  // (step = C: a thread has one column group)
+    s_sum[tid] = acc[0];
+    __syncthreads();
+    for (int k = 1; turn == 0 && k < turns; ++k) {
+      const float4 o = s_sum[tid + k * step * rp];
+      acc[0].x += o.x, acc[0].y += o.y, acc[0].z += o.z, acc[0].w += o.w;
+    }
+  }
+  if (r < R && turn == 0) {
+    const float inv = s_inv[r];
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (cg0 + k * step < C)
@@ -257,7 +313,7 @@ struct Split {
 static Split split_of(int n_max, int G, int d) {
   Split p;
   const int dp = d > 64 ? 128 : 64, tpt = kRows / G;
-  p.grid = device_sm_count();
+  p.grid = std::min(device_sm_count(), kMaxParts);
   p.rows = n_max <= tpt ? n_max * G : 2 * kRows;
   p.part_off = ((size_t)p.grid * 2 * sizeof(int4) + 255) / 256 * 256;
   p.ml_off = p.part_off + (size_t)p.grid * 2 * p.rows * dp * sizeof(float);
