@@ -152,16 +152,24 @@ def _check(rc: int, call: str):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_Tensor = torch.Tensor
+
+
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_get_device() if _get_device is not None and
+                               torch.cuda.is_initialized() else torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dev(t: torch.Tensor, dtype, numel: int, name: str) -> int:
     """Device pointer of a contiguous CUDA tensor holding at least `numel` elements."""
+    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and \
+            t.numel() >= numel:
+        return t.data_ptr() or None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -170,9 +178,7 @@ def _dev(t: torch.Tensor, dtype, numel: int, name: str) -> int:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"{name}: {t.numel()} elements, need {numel}")
-    return t.data_ptr() if numel > 0 else (t.data_ptr() or None)
+    raise ValueError(f"{name}: {t.numel()} elements, need {numel}")
 
 
 @dataclass
@@ -427,6 +433,10 @@ _IO = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 def _rows(t: torch.Tensor, dtype, T: int, heads: int, d: int, name: str):
     """(pointer, elements between rows) of a CUDA tensor [T][heads][d] whose rows may be views
     of longer ones (heads and elements contiguous)."""
+    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.shape == (T, heads, d):
+        s0, s1, s2 = t.stride()
+        if (s2 == 1 or d <= 1) and (s1 == d or heads <= 1):
+            return t.data_ptr(), s0 if T > 1 else heads * d
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -435,10 +445,7 @@ def _rows(t: torch.Tensor, dtype, T: int, heads: int, d: int, name: str):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != (T, heads, d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, heads, d)}")
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), s[0] if T > 1 else heads * d
+    raise ValueError(f"{name}: the heads of a row must be contiguous")
 
 
 def _io(t: torch.Tensor, name: str) -> int:
@@ -545,15 +552,18 @@ class Pages(_Handle):
                            device=self.table.device)
 
 
+_POOL_TYPES = (torch.bfloat16, torch.float16)
+
+
 def _pool(pages: Pages, pool: torch.Tensor) -> CPool:
-    if not isinstance(pool, torch.Tensor) or pool.dtype not in (torch.bfloat16, torch.float16):
+    if not isinstance(pool, _Tensor) or pool.dtype not in _POOL_TYPES:
         raise TypeError("pool: expected a bfloat16 or float16 tensor")
-    if pool.dim() != 6 or pool.shape[1] != 2 or pool.shape[2] != pages.n_pages or \
-            pool.shape[4] != pages.page_size:
-        raise ValueError(f"pool: shape {tuple(pool.shape)}, expected "
+    shape = pool.shape
+    if len(shape) != 6 or shape[1] != 2 or shape[2] != pages.n_pages or \
+            shape[4] != pages.page_size:
+        raise ValueError(f"pool: shape {tuple(shape)}, expected "
                          "(layers, 2, n_pages, H_kv, page_size, d)")
-    return CPool(pool.shape[0], pool.shape[3], pool.shape[5],
-                 _dev(pool, pool.dtype, pool.numel(), "pool"))
+    return CPool(shape[0], shape[3], shape[5], _dev(pool, pool.dtype, 0, "pool"))
 
 
 def pages_workspace_bytes(pages: Pages) -> int:
@@ -588,17 +598,25 @@ def pages_append(pages: Pages, cu, k, v, pool, path=None, n_path=None, advance: 
     one layer) to positions len[b], ...: the rows cu[b] .. cu[b+1] - 1, or with path
     [B][path_len] the rows cu[b] + path[b][i], i < n_path[b].  advance=False keeps len."""
     cp = _pool(pages, pool)
-    ptr = []
+    layers, H_kv, d = cp.layers, cp.H_kv, cp.d
+    if not isinstance(k, torch.Tensor) or k.dim() < 3:
+        raise ValueError(f"k: expected a tensor [{layers}][T][H_kv][d]")
+    T, ptr = k.shape[-3], []
     for t, name in ((k, "k"), (v, "v")):
         if isinstance(t, torch.Tensor) and t.dim() == 3:
             t = t.unsqueeze(0)
-        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != cp.layers:
-            raise ValueError(f"{name}: expected a tensor [{cp.layers}][T][H_kv][d]")
-        p, row = _rows(t[0], pool.dtype, k.shape[-3], cp.H_kv, cp.d, name)
-        ptr += [p, t.stride(0) if cp.layers > 1 else 0, row]
+        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != layers:
+            raise ValueError(f"{name}: expected a tensor [{layers}][T][H_kv][d]")
+        s = t.stride()
+        if t.is_cuda and t.dtype is pool.dtype and t.shape == (layers, T, H_kv, d) and layers and \
+                (s[3] == 1 or d <= 1) and (s[2] == d or H_kv <= 1):
+            p, row = t.data_ptr(), s[1] if T > 1 else H_kv * d
+        else:  # (says what is wrong)
+            p, row = _rows(t[0], pool.dtype, T, H_kv, d, name)
+        ptr += [p, s[0] if layers > 1 else 0, row]
     plen = 0 if path is None else path.shape[1]
     i32, B = torch.int32, pages.B
-    _check(lib().tgdn_pages_append(ctypes.byref(pages.c()), ctypes.byref(cp), k.shape[-3],
+    _check(lib().tgdn_pages_append(ctypes.byref(pages.c()), ctypes.byref(cp), T,
                                    _dev(cu, i32, B + 1, "cu"),
                                    None if path is None else _dev(path, i32, B * plen, "path"), plen,
                                    None if path is None else _dev(n_path, i32, B, "n_path"),
