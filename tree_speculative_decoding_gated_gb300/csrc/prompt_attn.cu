@@ -184,8 +184,8 @@ constexpr int kAltTokens = 768;
 template <int DP, typename E>
 static cudaError_t launch(const Args& a, const CUtensorMap& q, const CUtensorMap& k,
                           const CUtensorMap& v, int grid, cudaStream_t s) {
-  const bool alt = a.tiles == 1 && a.T / a.B >= kAltTokens;
-  const auto kern = alt ? prompt_attn_kernel<DP, E, true> : prompt_attn_kernel<DP, E, false>;
+  const auto kern = a.tiles == 1 && a.T / a.B >= kAltTokens ?
+                        prompt_attn_kernel<DP, E, true> : prompt_attn_kernel<DP, E, false>;
   constexpr int smem = smem_bytes<DP, false>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -216,10 +216,14 @@ cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, f
   a.o_wide = wide_rows(o, o_stride, d);
   a.v = v_rows;
   a.v_stride = v_stride;
-  // at most T / blk + B blocks per head; one row tile per item when two would leave SMs idle
+  // At most T / blk + B blocks per head.  One row tile per item when two would leave SMs idle,
+  // and with small heads, whose alternating pipelines lose least, while items are few: 5000
+  // tokens, 16 heads of 64 elements 67 us after 76, 16000 tokens, 4 heads 148 after 186; at
+  // d = 128 the same rule loses (9000 tokens 265 us after 219), and so do short prompts (20 of
+  // up to 1200 tokens, d = 64, 32.6 after 29.7).
   const int sms = device_sm_count();
   auto items = [&](int tiles) { return ((long)T / (a.tpt * tiles) + B) * H_kv; };
-  a.tiles = items(2) >= sms ? 2 : 1;
+  a.tiles = items(2) >= (d <= 64 && T / B >= kAltTokens ? 4 : 1) * sms ? 2 : 1;
   const long n = items(a.tiles);
   if (n > 0x3fffffffL) return cudaErrorInvalidConfiguration;
   const int grid = (int)n;
