@@ -249,7 +249,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // A value that all lanes of the warp hold, so that code depending on it is compiled as
 // warp-uniform (addresses and descriptors in uniform registers).
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x, int from = 0) {
+  return __shfl_sync(0xffffffffu, x, from);
+}
 
 // Tensor-core instructions of a convergent warp, issued by its elected lane (the same lane
 // every time).  Elected in place, four to an asm block with the descriptors' low words added
@@ -297,6 +299,18 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// A tensor copy by the elected lane of a convergent warp (26 cycles each; from a branch over
+// lanes 51, and then 16 boxes of 16 positions took longer than the products on them).
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, uint32_t bar, int x,
+                                         int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(to),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -381,7 +395,8 @@ __device__ __noinline__ float nonfinite_sum(const Args* a, const Seg* s, int tok
 // ------------------------------------------------------------------ the pipeline
 // W: the work list of this CTA; `bool next(Seg&)` is called by every lane of the copy warp.
 // ALT: items of one row tile may give their key tiles to the two pipelines in turn (prompts).
-template <int DP, typename E, bool PAGED, bool ALT, typename W>
+// P16: pages of 16 positions.
+template <int DP, typename E, bool PAGED, bool ALT, bool P16, typename W>
 __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUtensorMap* qmap,
                                          const CUtensorMap* kmap, const CUtensorMap* vmap,
                                          const CUtensorMap* kpmap, const CUtensorMap* vpmap) {
@@ -491,9 +506,20 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           const int np = min(ppt, (left + a.ps - 1) / a.ps);
           if (lane == 0) mbar_arrive_expect_tx(bar, np * prow * 128 * L::kHalves);
           __syncwarp();
-          if (lane < np) {
+          const int z = pg * a.H_kv + s.hk;
+          if (P16 && np == kKeys / 16) {
+            // (17- and 129-node trees over up to 8100 positions 221 us after 239; in the kernel
+            // for all page sizes the larger ones lost 1-2%)
+            const uint32_t to = uniform(smem_addr(dst)), b = uniform(smem_addr(bar));
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i) {
+              const int zi = uniform(z, i);
+#pragma unroll
+              for (int h = 0; h < L::kHalves; ++h)
+                copy_box(to + h * L::kHalf + i * 16 * 128, m, b, h * 64, 0, zi);
+            }
+          } else if (lane < np) {
             const int in = a.ps > kKeys ? (u * kKeys) % a.ps : 0;
-            const int z = pg * a.H_kv + s.hk;
 #pragma unroll
             for (int h = 0; h < L::kHalves; ++h)
               tma_load_3d(dst + h * L::kHalf + lane * prow * 128, m, bar, h * 64, in, z);

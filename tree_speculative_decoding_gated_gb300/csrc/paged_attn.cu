@@ -181,7 +181,7 @@ struct PagedWork {
   }
 };
 
-template <int DP, typename E>
+template <int DP, typename E, bool P16>
 __global__ void __launch_bounds__(kBlock, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap,
@@ -191,7 +191,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   extern __shared__ uint8_t pg_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(pg_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  pipeline<DP, E, true, false, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
+  pipeline<DP, E, true, false, P16, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.y's run and goes on into later
@@ -338,7 +338,7 @@ template <int DP, typename E>
 static cudaError_t launch(const Args& a, int grid, const CUtensorMap& q, const CUtensorMap& k,
                           const CUtensorMap& v, const CUtensorMap& kp, const CUtensorMap& vp,
                           cudaStream_t s) {
-  const auto kern = paged_attn_kernel<DP, E>;
+  const auto kern = a.ps == 16 ? paged_attn_kernel<DP, E, true> : paged_attn_kernel<DP, E, false>;
   constexpr int smem = smem_bytes<DP, true>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -179,7 +179,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   extern __shared__ uint8_t pa_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(pa_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  pipeline<DP, E, false, ALT, PromptWork>(smem, a, &qmap, &kmap, &vmap, nullptr, nullptr);
+  pipeline<DP, E, false, ALT, false, PromptWork>(smem, a, &qmap, &kmap, &vmap, nullptr, nullptr);
 }
 
 // Single row tiles whose key tiles alternate between the pipelines, from this mean length on:
