@@ -12,6 +12,7 @@
 // 33 rows 3.1 us, a launch and two rounds of loads.
 #include <cuda_fp16.h>
 
+#include "launch_after.cuh"
 #include "tgdn_device.cuh"
 #include "tgdn_kernels.h"
 
@@ -146,6 +147,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
   constexpr int V = RopeIo<E>::V;
   __shared__ int64_t s_pos[kRopeRows];
   __shared__ int s_ok[kRopeRows];
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int tid = threadIdx.x, t0 = blockIdx.x * rows;
   const int heads = a.H_q + a.H_kv, half = a.rot / 2;
   const int turned = PAIRS ? a.rot / V : half / V, copied = a.rot / V;  // units; first copied piece
@@ -228,6 +231,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const RopeArgs a
   extern __shared__ __align__(16) float2 turn[];
   __shared__ int64_t s_pos[kRopeRows];
   __shared__ int s_ok[kRopeRows];
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int tid = threadIdx.x, t0 = blockIdx.x * rows;
   rope_table(a, t0, rows, turn, s_pos, s_ok);
   const int heads = a.H_q + a.H_kv, half = a.rot / 2;
@@ -263,8 +268,7 @@ static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
   const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);
   const auto kern = !pieces ? rope_any_kernel<E> : pairs ? rope_kernel<E, true> : rope_kernel<E, false>;
-  kern<<<grid, kRopeThreads, smem, s>>>(a, rows);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(grid), dim3(kRopeThreads), smem, s, a, rows);
 }
 
 cudaError_t launch_rope(const RopeArgs& a, int io, cudaStream_t s) {

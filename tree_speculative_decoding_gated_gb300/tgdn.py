@@ -132,6 +132,23 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_calls = None
+
+
+def _native():
+    """The attention-layer calls' tensor marshalling in C++ (csrc/binding.cpp)."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise RuntimeError("_calls.so is missing or does not load: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _calls = module
+    return _calls
+
+
 def header_functions() -> list[str]:
     """Names of the functions include/tgdn.h declares."""
     text = open(HEADER).read()
@@ -427,33 +444,6 @@ def verify_noalloc(tree: Tree, dims: Dims, q, k, v, g, b, S0, o, stream=None) ->
 
 
 # ---------------------------------------------------------------- attention layers
-_IO = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-
-
-def _rows(t: torch.Tensor, dtype, T: int, heads: int, d: int, name: str):
-    """(pointer, elements between rows) of a CUDA tensor [T][heads][d] whose rows may be views
-    of longer ones (heads and elements contiguous)."""
-    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.shape == (T, heads, d):
-        s0, s1, s2 = t.stride()
-        if (s2 == 1 or d <= 1) and (s1 == d or heads <= 1):
-            return t.data_ptr(), s0 if T > 1 else heads * d
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor (the library takes device pointers)")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != (T, heads, d):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, heads, d)}")
-    raise ValueError(f"{name}: the heads of a row must be contiguous")
-
-
-def _io(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype not in _IO or t.dim() != 3:
-        raise TypeError(f"{name}: expected a float32, bfloat16 or float16 tensor [T][heads][d]")
-    return _IO[t.dtype]
-
-
 def rope_freqs(rot: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                orig_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
     """tgdn_rope_freqs: (freq, mscale) for rope().  freq [rot / 2] on `device`: each pair's turns
@@ -475,24 +465,8 @@ def rope(q, k, q_out, k_out, freq, *, cu, base=None, off=None, interleaved: bool
     of each head are rotated.  Row t of sequence b (cu [B + 1] int32) is at position
     base[b] + off[t] (int32; default: its index within the sequence).  transpose=True is the
     gradient."""
-    io = _io(q, "q")
-    T, H_q, d = q.shape
-    H_kv = 0 if k is None else k.shape[1]
-    B = cu.numel() - 1
-    qp, qs = _rows(q, q.dtype, T, H_q, d, "q")
-    qop, qos = _rows(q_out, q.dtype, T, H_q, d, "q_out")
-    kp = kop = None
-    ks = kos = 0
-    if k is not None:
-        kp, ks = _rows(k, q.dtype, T, H_kv, d, "k")
-        kop, kos = _rows(k_out, q.dtype, T, H_kv, d, "k_out")
-    i32 = torch.int32
-    _check(lib().tgdn_rope(B, T, H_q, H_kv, d, 2 * freq.numel(), int(interleaved), int(transpose),
-                           io, mscale, _dev(freq, torch.int64, freq.numel(), "freq"),
-                           _dev(cu, i32, B + 1, "cu"),
-                           None if base is None else _dev(base, i32, B, "base"),
-                           None if off is None else _dev(off, i32, T, "off"),
-                           qp, qs, kp, ks, qop, qos, kop, kos, _stream(stream)), "tgdn_rope")
+    _check(_native().rope(q, k, q_out, k_out, freq, cu, base, off, interleaved, mscale, transpose,
+                          stream), "tgdn_rope")
 
 
 def prompt_attention_workspace_bytes(B: int, T: int, H_q: int, H_kv: int, d: int) -> int:
@@ -503,25 +477,8 @@ def prompt_attention(cu, q, k, v, o, scale: float, status, ws=None, stream=None)
     """tgdn_prompt_attention: causal attention over whole prompts packed one after another
     (cu [B + 1] int32).  q, o [T][H_q][d], k, v [T][H_kv][d] (bf16 or f16; rows may be views of
     a fused projection); status [B] int32 is written."""
-    io = _io(q, "q")
-    T, H_q, d = q.shape
-    H_kv = k.shape[1]
-    B = cu.numel() - 1
-    qp, qs = _rows(q, q.dtype, T, H_q, d, "q")
-    kp, ks = _rows(k, q.dtype, T, H_kv, d, "k")
-    vp, vs = _rows(v, q.dtype, T, H_kv, d, "v")
-    op, os_ = _rows(o, q.dtype, T, H_q, d, "o")
-    wsp, wsn = _workspace(ws)
-    _check(lib().tgdn_prompt_attention(B, T, H_q, H_kv, d, io, _dev(cu, torch.int32, B + 1, "cu"),
-                                       qp, qs, kp, ks, vp, vs, scale, op, os_,
-                                       _dev(status, torch.int32, B, "status"), wsp, wsn,
-                                       _stream(stream)), "tgdn_prompt_attention")
-
-
-def _workspace(ws):
-    if ws is None or ws.numel() == 0:
-        return None, 0
-    return _dev(ws, ws.dtype, ws.numel(), "ws"), ws.numel() * ws.element_size()
+    _check(_native().prompt_attention(cu, q, k, v, o, scale, status, ws, stream),
+           "tgdn_prompt_attention")
 
 
 class Pages(_Handle):
@@ -552,20 +509,6 @@ class Pages(_Handle):
                            device=self.table.device)
 
 
-_POOL_TYPES = (torch.bfloat16, torch.float16)
-
-
-def _pool(pages: Pages, pool: torch.Tensor) -> CPool:
-    if not isinstance(pool, _Tensor) or pool.dtype not in _POOL_TYPES:
-        raise TypeError("pool: expected a bfloat16 or float16 tensor")
-    shape = pool.shape
-    if len(shape) != 6 or shape[1] != 2 or shape[2] != pages.n_pages or \
-            shape[4] != pages.page_size:
-        raise ValueError(f"pool: shape {tuple(shape)}, expected "
-                         "(layers, 2, n_pages, H_kv, page_size, d)")
-    return CPool(shape[0], shape[3], shape[5], _dev(pool, pool.dtype, 0, "pool"))
-
-
 def pages_workspace_bytes(pages: Pages) -> int:
     return int(lib().tgdn_pages_workspace_bytes(ctypes.byref(pages.c())))
 
@@ -578,18 +521,9 @@ def pages_workspace(pages: Pages) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=pages.table.device)
 
 
-def _pages_ws(pages: Pages, ws) -> int:
-    d = pages.__dict__
-    if d["_struct"] is None or "_ws" not in d:
-        d["_ws"] = pages_workspace_bytes(pages)  # depends on the sizes alone
-    return _dev(ws, torch.uint8, d["_ws"], "ws")
-
-
 def pages_reserve(pages: Pages, add, ws, stream=None) -> None:
     """tgdn_pages_reserve: pages for add[b] more positions of every sequence (int32 [B])."""
-    _check(lib().tgdn_pages_reserve(ctypes.byref(pages.c()),
-                                    _dev(add, torch.int32, pages.B, "add"), _pages_ws(pages, ws),
-                                    _stream(stream)), "tgdn_pages_reserve")
+    _check(_native().pages_reserve(pages, add, ws, stream), "tgdn_pages_reserve")
 
 
 def pages_append(pages: Pages, cu, k, v, pool, path=None, n_path=None, advance: bool = True,
@@ -597,53 +531,23 @@ def pages_append(pages: Pages, cu, k, v, pool, path=None, n_path=None, advance: 
     """tgdn_pages_append: keys and values k, v [layers][T][H_kv][d] (or [T][H_kv][d] for a pool of
     one layer) to positions len[b], ...: the rows cu[b] .. cu[b+1] - 1, or with path
     [B][path_len] the rows cu[b] + path[b][i], i < n_path[b].  advance=False keeps len."""
-    cp = _pool(pages, pool)
-    layers, H_kv, d = cp.layers, cp.H_kv, cp.d
-    if not isinstance(k, torch.Tensor) or k.dim() < 3:
-        raise ValueError(f"k: expected a tensor [{layers}][T][H_kv][d]")
-    T, ptr = k.shape[-3], []
-    for t, name in ((k, "k"), (v, "v")):
-        if isinstance(t, torch.Tensor) and t.dim() == 3:
-            t = t.unsqueeze(0)
-        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != layers:
-            raise ValueError(f"{name}: expected a tensor [{layers}][T][H_kv][d]")
-        s = t.stride()
-        if t.is_cuda and t.dtype is pool.dtype and t.shape == (layers, T, H_kv, d) and layers and \
-                (s[3] == 1 or d <= 1) and (s[2] == d or H_kv <= 1):
-            p, row = t.data_ptr(), s[1] if T > 1 else H_kv * d
-        else:  # (says what is wrong)
-            p, row = _rows(t[0], pool.dtype, T, H_kv, d, name)
-        ptr += [p, s[0] if layers > 1 else 0, row]
-    plen = 0 if path is None else path.shape[1]
-    i32, B = torch.int32, pages.B
-    _check(lib().tgdn_pages_append(ctypes.byref(pages.c()), ctypes.byref(cp), T,
-                                   _dev(cu, i32, B + 1, "cu"),
-                                   None if path is None else _dev(path, i32, B * plen, "path"), plen,
-                                   None if path is None else _dev(n_path, i32, B, "n_path"),
-                                   *ptr, int(advance), _stream(stream)), "tgdn_pages_append")
+    _check(_native().pages_append(pages, cu, k, v, pool, path, n_path, advance, stream),
+           "tgdn_pages_append")
 
 
 def pages_fork(pages: Pages, src, dst, pool, status, ws, stream=None) -> None:
     """tgdn_pages_fork: sequence dst[i] becomes a copy of src[i] (int32 [n]); status [n] int32."""
-    n, i32 = src.numel(), torch.int32
-    _check(lib().tgdn_pages_fork(ctypes.byref(pages.c()), ctypes.byref(_pool(pages, pool)), n,
-                                 _dev(src, i32, n, "src"), _dev(dst, i32, n, "dst"),
-                                 _dev(status, i32, n, "status"), _pages_ws(pages, ws),
-                                 _stream(stream)), "tgdn_pages_fork")
+    _check(_native().pages_fork(pages, src, dst, pool, status, ws, stream), "tgdn_pages_fork")
 
 
 def pages_free(pages: Pages, seq, stream=None) -> None:
     """tgdn_pages_free: releases the pages of the listed sequences (int32)."""
-    _check(lib().tgdn_pages_free(ctypes.byref(pages.c()), seq.numel(),
-                                 _dev(seq, torch.int32, seq.numel(), "seq"), _stream(stream)),
-           "tgdn_pages_free")
+    _check(_native().pages_free(pages, seq, stream), "tgdn_pages_free")
 
 
 def pages_compact(pages: Pages, pool, n_live, ws, stream=None) -> None:
     """tgdn_pages_compact: live pages to the front of the pool; n_live [1] int32 is written."""
-    _check(lib().tgdn_pages_compact(ctypes.byref(pages.c()), ctypes.byref(_pool(pages, pool)),
-                                    _dev(n_live, torch.int32, 1, "n_live"), _pages_ws(pages, ws),
-                                    _stream(stream)), "tgdn_pages_compact")
+    _check(_native().pages_compact(pages, pool, n_live, ws, stream), "tgdn_pages_compact")
 
 
 def paged_tree_attention_workspace_bytes(tree: Tree, pages: Pages, H_q: int, H_kv: int,
@@ -658,22 +562,8 @@ def paged_tree_attention(tree: Tree, pages: Pages, q, k_tree, v_tree, k_pages, v
     projection), k_pages/v_pages [n_pages][H_kv][page_size][d] (one layer of the pool), bf16 or
     f16.  ws: optional workspace of paged_tree_attention_workspace_bytes() bytes, with which
     long contexts are split over CTAs."""
-    io = _io(q, "q")
-    T, H_q, d = q.shape
-    if T != tree.T:
-        raise ValueError(f"q: {T} rows, the tree has {tree.T}")
-    H_kv = k_tree.shape[1]
-    qp, qs = _rows(q, q.dtype, T, H_q, d, "q")
-    kp, ks = _rows(k_tree, q.dtype, T, H_kv, d, "k_tree")
-    vp, vs = _rows(v_tree, q.dtype, T, H_kv, d, "v_tree")
-    op, os_ = _rows(o, q.dtype, T, H_q, d, "o")
-    n = pages.n_pages * H_kv * pages.page_size * d
-    wsp, wsn = _workspace(ws)
-    _check(lib().tgdn_paged_tree_attention(ctypes.byref(tree.c()), ctypes.byref(pages.c()), H_q,
-                                           H_kv, d, io, qp, qs, kp, ks, vp, vs,
-                                           _dev(k_pages, q.dtype, n, "k_pages"),
-                                           _dev(v_pages, q.dtype, n, "v_pages"), scale, op, os_,
-                                           wsp, wsn, _stream(stream)), "tgdn_paged_tree_attention")
+    _check(_native().paged_tree_attention(tree, pages, q, k_tree, v_tree, k_pages, v_pages, o,
+                                          scale, ws, stream), "tgdn_paged_tree_attention")
 
 
 def debug_set_wait_hooks(wait_limit_ns: int = 0, withhold_item: int = -1) -> None:
