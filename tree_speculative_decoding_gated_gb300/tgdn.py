@@ -509,6 +509,16 @@ class Pages(_Handle):
                            device=self.table.device)
 
 
+def _pool(pages: Pages, pool: torch.Tensor) -> torch.Tensor:
+    """The pool, if it is one of these pages' kind (its device and layout are checked in C++)."""
+    if not isinstance(pool, torch.Tensor) or pool.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("pool: expected a bfloat16 or float16 tensor")
+    s = pool.shape
+    if len(s) != 6 or s[1] != 2 or s[2] != pages.n_pages or s[4] != pages.page_size:
+        raise ValueError(f"pool: shape {tuple(s)}, expected (layers, 2, n_pages, H_kv, page_size, d)")
+    return pool
+
+
 def pages_workspace_bytes(pages: Pages) -> int:
     return int(lib().tgdn_pages_workspace_bytes(ctypes.byref(pages.c())))
 
@@ -531,13 +541,15 @@ def pages_append(pages: Pages, cu, k, v, pool, path=None, n_path=None, advance: 
     """tgdn_pages_append: keys and values k, v [layers][T][H_kv][d] (or [T][H_kv][d] for a pool of
     one layer) to positions len[b], ...: the rows cu[b] .. cu[b+1] - 1, or with path
     [B][path_len] the rows cu[b] + path[b][i], i < n_path[b].  advance=False keeps len."""
-    _check(_native().pages_append(pages, cu, k, v, pool, path, n_path, advance, stream),
+    _check(_native().pages_append(pages, cu, k, v, _pool(pages, pool), path, n_path, advance,
+                                  stream),
            "tgdn_pages_append")
 
 
 def pages_fork(pages: Pages, src, dst, pool, status, ws, stream=None) -> None:
     """tgdn_pages_fork: sequence dst[i] becomes a copy of src[i] (int32 [n]); status [n] int32."""
-    _check(_native().pages_fork(pages, src, dst, pool, status, ws, stream), "tgdn_pages_fork")
+    _check(_native().pages_fork(pages, src, dst, _pool(pages, pool), status, ws, stream),
+           "tgdn_pages_fork")
 
 
 def pages_free(pages: Pages, seq, stream=None) -> None:
@@ -547,7 +559,8 @@ def pages_free(pages: Pages, seq, stream=None) -> None:
 
 def pages_compact(pages: Pages, pool, n_live, ws, stream=None) -> None:
     """tgdn_pages_compact: live pages to the front of the pool; n_live [1] int32 is written."""
-    _check(_native().pages_compact(pages, pool, n_live, ws, stream), "tgdn_pages_compact")
+    _check(_native().pages_compact(pages, _pool(pages, pool), n_live, ws, stream),
+           "tgdn_pages_compact")
 
 
 def paged_tree_attention_workspace_bytes(tree: Tree, pages: Pages, H_q: int, H_kv: int,
