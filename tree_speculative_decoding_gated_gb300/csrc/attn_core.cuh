@@ -68,10 +68,11 @@ constexpr float kGap = 8.f;  // lazy rescaling threshold (natural log units)
 constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (128 each), O_0, O_1 (128 each)
 constexpr int kMaxNodes = TGDN_MAX_NODES;
 
-// Shared-memory layout for heads padded to DP = 64 or 128 elements.
+// Shared-memory layout for heads padded to DP = 64, 96 or 128 elements (96: 8192 tokens with
+// d = 96 155 us after 186 as 128; tiles are laid out as for 128).
 template <int DP, bool PAGED>
 struct Lay {
-  static constexpr int kHalves = DP / 64;               // 128-byte swizzled halves of a row
+  static constexpr int kHalves = (DP + 63) / 64;               // 128-byte swizzled halves of a row
   static constexpr int kHalf = kKeys * 128;             // one half of a tile
   static constexpr int kTile = kHalf * kHalves;         // a key, value or query tile
   // key and value tiles in flight: what shared memory holds (paged: beside the masks)
@@ -276,7 +277,19 @@ __device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint
       "r"(a), "r"(b), "r"(id), "r"(add), "r"(kDescHi)
       : "memory");
 }
-// The same over 64 keys with A (16-bit pairs, 8 columns per k-step) in tensor memory and B
+// Two k-steps of them, D += A B.
+__device__ __forceinline__ void mma_ss2(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred t, e;\n\t.reg .b32 u, v;\n\t.reg .b64 x, y;\n\t"
+      "setp.eq.b32 t, %3, %3;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.u32 u, %1, 2;\n\tadd.u32 v, %2, 2;\n\tmov.b64 x, {u, %4};\n\tmov.b64 y, {v, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHi)
+      : "memory");
+}
+// Four over 64 keys with A (16-bit pairs, 8 columns per k-step) in tensor memory and B
 // MN-major (2048 bytes per k-step).
 __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
                                         uint32_t add) {
@@ -638,8 +651,11 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       tc_fence_after_sync();
       const uint32_t q = dQ + rows * (L::kTile >> 4), k = dK + slot * (L::kTile >> 4);
 #pragma unroll
-      for (int h = 0; h < L::kHalves; ++h)
-        mma_ss4(utm + t * 128, q + h * (L::kHalf >> 4), k + h * (L::kHalf >> 4), id_s, h);
+      for (int h = 0; h < L::kHalves; ++h) {
+        const uint32_t qh = q + h * (L::kHalf >> 4), kh = k + h * (L::kHalf >> 4);
+        if (DP - h * 64 == 32) mma_ss2(utm + t * 128, qh, kh, id_s);
+        else mma_ss4(utm + t * 128, qh, kh, id_s, h);
+      }
       commit(b_s + t * 8);
     };
     // O_t (+)= P_t V of the step, 64 keys at a time as their P comes.  With P apart the next
@@ -1057,8 +1073,9 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           const float2 w = br->alt_ml[row];
           const bool dirty = *reinterpret_cast<volatile int*>(&br->dirty[r]) != 0;
           const uint32_t tO0 = tmem + L::kColO + lanes;
+          constexpr int kFirst = (DP / 32 + 1) / 2;  // pipeline 0's share, 32 columns apiece
 #pragma unroll 1
-          for (int q = t * (DP / 64); q < (t + 1) * (DP / 64); ++q) {
+          for (int q = t == 0 ? 0 : kFirst; q < (t == 0 ? kFirst : DP / 32); ++q) {
             __syncwarp();
             float o[32], x[32];
             tmem_ld32(tO0 + q * 32, o);

@@ -325,7 +325,7 @@ struct Split {
 };
 static Split split_of(int n_max, int G, int d) {
   Split p;
-  const int dp = d > 64 ? 128 : 64, tpt = kRows / G;
+  const int dp = d > 96 ? 128 : d > 64 ? 96 : 64, tpt = kRows / G;
   p.grid = std::min(device_sm_count(), kMaxParts);
   p.rows = n_max <= tpt ? n_max * G : 2 * kRows;
   p.part_off = ((size_t)p.grid * 2 * sizeof(int4) + 255) / 256 * 256;
@@ -395,11 +395,13 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml_off);
   }
-  if (d > 64)
-    return io == TGDN_BF16 ? launch<128, __nv_bfloat16>(a, p.grid, q, k, v, kp, vp, s)
-                           : launch<128, __half>(a, p.grid, q, k, v, kp, vp, s);
-  return io == TGDN_BF16 ? launch<64, __nv_bfloat16>(a, p.grid, q, k, v, kp, vp, s)
-                         : launch<64, __half>(a, p.grid, q, k, v, kp, vp, s);
+  auto go = [&](auto e) {
+    using E = decltype(e);
+    return d > 96 ? launch<128, E>(a, p.grid, q, k, v, kp, vp, s)
+         : d > 64 ? launch<96, E>(a, p.grid, q, k, v, kp, vp, s)
+                  : launch<64, E>(a, p.grid, q, k, v, kp, vp, s);
+  };
+  return io == TGDN_BF16 ? go(__nv_bfloat16()) : go(__half());
 }
 
 }  // namespace tgdn

@@ -233,11 +233,12 @@ cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, f
   const long n = items(a.tiles);
   if (n > 0x3fffffffL) return cudaErrorInvalidConfiguration;
   const int grid = (int)n;
-  if (d > 64)
-    return io == TGDN_BF16 ? launch<128, __nv_bfloat16>(a, q, k, v, grid, s)
-                           : launch<128, __half>(a, q, k, v, grid, s);
-  return io == TGDN_BF16 ? launch<64, __nv_bfloat16>(a, q, k, v, grid, s)
-                         : launch<64, __half>(a, q, k, v, grid, s);
+  auto go = [&](auto e) {
+    using E = decltype(e);
+    return d > 96 ? launch<128, E>(a, q, k, v, grid, s)
+         : d > 64 ? launch<96, E>(a, q, k, v, grid, s) : launch<64, E>(a, q, k, v, grid, s);
+  };
+  return io == TGDN_BF16 ? go(__nv_bfloat16()) : go(__half());
 }
 
 }  // namespace tgdn
