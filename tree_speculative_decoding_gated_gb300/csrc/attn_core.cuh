@@ -127,6 +127,7 @@ struct Args {
   float2* part_ml;
   int4* desc;                      // [grid][2]: the split item that begins in a CTA's range
   int part_rows;                   // rows per partial slot
+  int min_share;                   // least key tiles per CTA
 };
 
 // (o_wide of Args)

@@ -8,7 +8,7 @@
 // Decoding reads each cached key and value once for a handful of query rows, so memory
 // bounds it, and what costs is uneven lengths.  All key tiles of all items are therefore
 // numbered through and every CTA takes an equal run of them, wherever it begins and ends
-// (kMinShare at least: a cut costs a merge).  A run covers whole items and at most two
+// (kMinShare at least: a cut costs a join).  A run covers whole items and at most two
 // cut ones; the parts of a cut item (O unnormalised, reference maximum, sum) go to the
 // workspace and paged_merge_kernel joins them in order of their keys, so results do not
 // depend on timing.  Without a workspace items stay whole.
@@ -26,11 +26,13 @@
 namespace tgdn {
 namespace attn {
 
-// Key tiles per CTA below which a cut costs more than it saves: a tile takes ~0.9 us, a join ~4.
-constexpr int kMinShare = 4;
-// Caches that can hold no more key tiles than this are never cut (one token over 300 positions:
-// 11 us whole, 14 in two).
-constexpr int kSplitTiles = 6;
+// Key tiles per CTA below which a cut costs more than it saves, and caches that can hold no more
+// key tiles than kSplitTiles are never cut: parts of many rows take long to write and join (8
+// heads of 200 nodes over 3000 positions: shares of 4 tiles 30 us, 2 tiles 40), parts of up to
+// kFewRows do not (one token over 1000 positions 14.2 and 12.1; over 600 13.3 whole, 12.3 cut;
+// over 300 11.1 whole, 11.8 cut).
+constexpr int kFewRows = 8;
+constexpr int kMinShare[2] = {4, 2}, kSplitTiles[2] = {6, 4};  // [few rows]
 // An item's start and output, in key tiles (0: 64-node trees over 4096 positions 35.2 us, 1: 33.5,
 // 2: 31.5).
 constexpr int kItemCost = 2;
@@ -108,7 +110,7 @@ struct PagedWork {
       sum += __shfl_sync(0xffffffffu, warp_sum_upto(more, lane), 31);
     }
     share = divide(sum + gridDim.x - 1, gridDim.x);
-    if (share < kMinShare) share = kMinShare;
+    if (share < a.min_share) share = a.min_share;
     x = min(sum, share * blockIdx.x);
     x1 = min(sum, x + share);
     d0 = make_int4(-1, 0, 0, 0);
@@ -390,7 +392,9 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   a.part_rows = p.rows;
   // a short cache is not split: the merge would take longer than the tiles it spares
   const int64_t most = ((int64_t)pg.max_pages * pg.page_size + kKeys - 1) / kKeys + (t.n_max + kKeys - 1) / kKeys;
-  if (ws != nullptr && ws_bytes >= p.bytes && most > kSplitTiles) {
+  const bool few = p.rows <= kFewRows;
+  a.min_share = kMinShare[few];
+  if (ws != nullptr && ws_bytes >= p.bytes && most > kSplitTiles[few]) {
     a.desc = static_cast<int4*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml_off);
