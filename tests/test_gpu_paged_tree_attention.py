@@ -144,6 +144,18 @@ def test_long_context_in_many_parts():
         c.check(c.run(split))
 
 
+@pytest.mark.parametrize("nodes,lens,H_q,H_kv,d", [
+    ([33, 12, 0, 5], [9000, 6001, 50, 0], 4, 1, 128),      # two row tiles, few items
+    ([7, 3], [9500, 5000], 8, 2, 96),                       # 28 rows, joined eight at a time
+    ([1, 1, 2], [12000, 1, 7777], 5, 1, 64),                # few rows in all
+    ([64] * 9, [1500] * 8 + [900], 16, 4, 128)])            # many items, 32 rows at a time
+def test_joins_of_every_kind(nodes, lens, H_q, H_kv, d):
+    c = Case(trees(np.random.default_rng(12), nodes), lens, H_q, H_kv, d, 64, BF, seed=13)
+    o = c.run(True)
+    c.check(o)
+    assert torch.equal(o, c.run(True))
+
+
 def test_many_sequences():
     rng = np.random.default_rng(6)
     B = 70

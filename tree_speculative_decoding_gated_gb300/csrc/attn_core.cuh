@@ -128,6 +128,7 @@ struct Args {
   int4* desc;                      // [grid][2]: the split item that begins in a CTA's range
   int part_rows;                   // rows per partial slot
   int min_share;                   // least key tiles per CTA
+  int runs, joins;                 // CTAs of the attention kernel; of a narrow join per row group
 };
 
 // (o_wide of Args)

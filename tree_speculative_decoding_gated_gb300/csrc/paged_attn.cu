@@ -196,34 +196,64 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   pipeline<DP, E, true, false, P16, PagedWork>(smem, a, &qmap, &kmap, &vmap, &kpmap, &vpmap);
 }
 
-// Joins the parts of the item that begins in CTA blockIdx.y's run and goes on into later
-// ones, 32 query rows per CTA:
+// Joins the parts of an item that begins in one run and goes on into later ones, a row group
+// (32 query rows, or 8) per CTA:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
-// First the weights, a lane per part, so that all statistics are under way at once; then
-// the sums, a thread per row and four columns, whose loads wait for nothing.  What few rows
-// leave of the CTA takes parts in turn.  One token over 40000 positions (35 parts of 4 rows):
-// call 40.6 -> 30.5 us against one thread passing over all parts.
-constexpr int kMergeRows = 32;
+// First the weights, several lanes per row, so that all statistics are under way at once;
+// then the sums, a thread per row and four columns, whose loads wait for nothing.
+//   32 rows: one CTA per row group and run; those of runs that name no item leave at once.
+//   8 rows (NARROW): rows that are no more, or few items, whose CTAs seek out their runs; what
+//   few rows leave of a CTA takes parts in turn.  More parts are under way and more CTAs
+//   share an item: 33-node trees over 34400 positions (7 items of ~25 parts) 107 -> 29 us a
+//   call, 7-node ones over 9696 30.8 -> 16.1; where items are many the CTAs cost more than
+//   they save (8 trees of 64 nodes over 1000 positions, 32 items, 19.7 -> 25.6).
+constexpr int kMergeRows = 32, kNarrowRows = 8;
 constexpr int kMaxParts = 160;
-template <int DP, typename E>
+template <int DP, typename E, bool NARROW>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ Args a) {
-  __shared__ float s_w[kMaxParts][kMergeRows];
-  __shared__ float s_inv[kMergeRows];
+  constexpr int kGroup = NARROW ? kNarrowRows : kMergeRows;
+  __shared__ float s_w[kMaxParts][kGroup];
+  __shared__ float s_inv[kGroup];
   __shared__ float4 s_sum[256];
-  __shared__ __align__(16) uint8_t s_out[kMergeRows][DP * 2 + 16];
+  __shared__ __align__(16) uint8_t s_out[kGroup][DP * 2 + 16];
   grid_dependency_wait();
-  const int c = blockIdx.y, tid = threadIdx.x;  // (an item's row groups go to different SMs)
-  const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
-  if (d0.x < 0) return;
-  const int r0 = blockIdx.x * kMergeRows, R = min(kMergeRows, a.part_rows - r0);
+  const int tid = threadIdx.x;
+  int c = blockIdx.y;  // (an item's row groups go to different SMs)
+  int4 d0, d1;
+  if (!NARROW || gridDim.y == a.runs) {
+    d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
+    if (d0.x < 0) return;
+  } else {  // the blockIdx.y-th run that names a cut item
+    __shared__ int s_run;
+    if (tid < 32) {
+      int x[kMaxParts / 32], left = c, run = -1;
+#pragma unroll
+      for (int j = 0; j < kMaxParts / 32; ++j)
+        x[j] = j * 32 + tid < a.runs ? a.desc[2 * (j * 32 + tid)].x : -1;
+#pragma unroll
+      for (int j = 0; j < kMaxParts / 32; ++j) {
+        const uint32_t cut = __ballot_sync(0xffffffffu, x[j] >= 0);
+        if (x[j] >= 0 && __popc(cut & ((1u << tid) - 1)) == left) run = j * 32 + tid;
+        left -= __popc(cut);
+      }
+      run = __reduce_max_sync(0xffffffffu, run);
+      if (tid == 0) s_run = run;
+    }
+    __syncthreads();
+    c = s_run;
+    if (c < 0) return;
+    d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
+  }
+  const int r0 = blockIdx.x * kGroup, R = min(kGroup, a.part_rows - r0);
   if ((r0 / kRows) * a.tpt + d0.w >= d0.z) return;  // no row of this row tile exists
   // part i lies in CTA c + i's first slot, the first part in the slot its CTA named
   const int parts = min(d1.y - c + 1, kMaxParts);
   auto slot = [&](int i) -> int64_t { return 2 * (c + i) + (i == 0 ? d1.z : 0); };
   int rp = 1;  // threads side by side over rows: the power of two from R up
   while (rp < R) rp *= 2;
-  constexpr int C = DP / 4, kPer = C / 8;      // column groups; the most of one thread
-  constexpr int kNext = 4;                     // parts under way
+  constexpr int C = DP / 4;                    // column groups
+  constexpr int kPer = NARROW ? 1 : C / 8;     // of them, the most of one thread
+  constexpr int kNext = NARROW ? 16 : 4;       // parts under way
   const int r = tid & (rp - 1), over = tid / rp;
   const int step = min(256 / rp, C);           // threads over the columns
   const int turns = 256 / rp / step;           // and over the parts
@@ -244,25 +274,26 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   {
     const int sub = min(32, 256 / rp), rw = tid / sub, i0 = tid % sub;  // sub lanes per row
     const float2* ml = a.part_ml + r0 + min(rw, R - 1);
-    float2 v[kNext];  // (all there are, but for many parts of many rows)
+    constexpr int kStat = 4;
+    float2 v[kStat];  // (all there are, but for many parts of many rows)
     float M = -INFINITY, sum = 0.f;
-    for (int b = i0; b < parts; b += kNext * sub) {
+    for (int b = i0; b < parts; b += kStat * sub) {
 #pragma unroll
-      for (int j = 0; j < kNext; ++j) {
+      for (int j = 0; j < kStat; ++j) {
         const int i = b + j * sub;
         v[j] = i < parts ? ml[slot(i) * a.part_rows] : make_float2(0.f, 0.f);
       }
 #pragma unroll
-      for (int j = 0; j < kNext; ++j)
+      for (int j = 0; j < kStat; ++j)
         if (v[j].y != 0.f) M = fmaxf(M, v[j].x);
     }
     for (int o = sub / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int b = i0; b < parts; b += kNext * sub) {
+    for (int b = i0; b < parts; b += kStat * sub) {
 #pragma unroll
-      for (int j = 0; j < kNext; ++j) {
+      for (int j = 0; j < kStat; ++j) {
         const int i = b + j * sub;
         if (i >= parts) continue;
-        if (parts > kNext * sub) v[j] = ml[slot(i) * a.part_rows];
+        if (parts > kStat * sub) v[j] = ml[slot(i) * a.part_rows];
         const float w = v[j].y == 0.f ? 0.f : fast_exp2(v[j].x - M);
         sum = fmaf(w, v[j].y, sum);
         if (rw < R) s_w[i][rw] = w;
@@ -329,7 +360,7 @@ static Split split_of(int n_max, int G, int d) {
   Split p;
   const int dp = d > 96 ? 128 : d > 64 ? 96 : 64, tpt = kRows / G;
   p.grid = std::min(device_sm_count(), kMaxParts);
-  p.rows = n_max <= tpt ? n_max * G : 2 * kRows;
+  p.rows = n_max <= tpt ? std::max(n_max, 1) * G : 2 * kRows;
   p.part_off = ((size_t)p.grid * 2 * sizeof(int4) + 255) / 256 * 256;
   p.ml_off = p.part_off + (size_t)p.grid * 2 * p.rows * dp * sizeof(float);
   p.bytes = p.ml_off + (size_t)p.grid * 2 * p.rows * sizeof(float2);
@@ -346,8 +377,11 @@ static cudaError_t launch(const Args& a, int grid, const CUtensorMap& q, const C
   if (e != cudaSuccess) return e;
   e = launch_after(kern, dim3(grid), dim3(kBlock), smem, s, q, k, v, kp, vp, a);
   if (e != cudaSuccess || a.part == nullptr) return e;
-  return launch_after(paged_merge_kernel<DP, E>, dim3((a.part_rows + kMergeRows - 1) / kMergeRows, grid), dim3(256), 0, s,
-                      a);
+  if (a.joins > 0)  // (few rows in all, or few items)
+    return launch_after(paged_merge_kernel<DP, E, true>,
+                        dim3((a.part_rows + kNarrowRows - 1) / kNarrowRows, a.joins), dim3(256), 0, s, a);
+  return launch_after(paged_merge_kernel<DP, E, false>,
+                      dim3((a.part_rows + kMergeRows - 1) / kMergeRows, grid), dim3(256), 0, s, a);
 }
 
 }  // namespace attn
@@ -390,6 +424,11 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   a.held = pg.held;
   const Split p = split_of(t.n_max, a.G, d);
   a.part_rows = p.rows;
+  a.runs = p.grid;
+  // (few items: no more than four joining CTAs per SM)
+  const int64_t items = (int64_t)t.B * H_kv * ((t.n_max + 2 * a.tpt - 1) / (2 * a.tpt));
+  if (p.rows <= kNarrowRows) a.joins = p.grid;
+  else if (items * ((p.rows + kNarrowRows - 1) / kNarrowRows) <= 4 * p.grid) a.joins = std::max((int)items, 1);
   // a short cache is not split: the merge would take longer than the tiles it spares
   const int64_t most = ((int64_t)pg.max_pages * pg.page_size + kKeys - 1) / kKeys + (t.n_max + kKeys - 1) / kKeys;
   const bool few = p.rows <= kFewRows;
