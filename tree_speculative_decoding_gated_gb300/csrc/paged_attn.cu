@@ -14,7 +14,7 @@
 // depend on timing.  Without a workspace items stay whole.
 //
 // Measured: single tokens over up to 131072 positions (8 sequences, 2 heads of 128, fp16)
-// 106 us for 622 MB, 88% of the copy bandwidth.  64-node trees over up to 4096 positions
+// 104 us for 622 MB, 89% of the copy bandwidth.  64-node trees over up to 4096 positions
 // (16 sequences) 31 us for 65 MB: start, one cut and the join, ~12 us, weigh as much as
 // the tiles.  A batch of 17- and 129-node trees over up to 8100 positions 220 us: 129 nodes
 // of four heads are five row tiles in three blocks, whose reads of the same keys lie apart
