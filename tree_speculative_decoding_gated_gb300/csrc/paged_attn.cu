@@ -26,13 +26,14 @@
 namespace tgdn {
 namespace attn {
 
-// Key tiles per CTA below which a cut costs more than it saves, and caches that can hold no more
-// key tiles than kSplitTiles are never cut: parts of many rows take long to write and join (8
-// heads of 200 nodes over 3000 positions: shares of 4 tiles 30 us, 2 tiles 40), parts of up to
-// kFewRows do not (one token over 1000 positions 14.2 and 12.1; over 600 13.3 whole, 12.3 cut;
-// over 300 11.1 whole, 11.8 cut).
+// Key tiles per CTA below which a cut costs more than it saves: two where the parts are joined
+// eight rows at a time (7-node trees over 1500 positions 14.8 and 12.7 us, 4 trees of 64 nodes
+// over 4000 23.0 and 20.9), four else.  Caches that can hold no more key tiles than kSplitTiles
+// are never cut: 6, or 4 for up to kFewRows rows (one token over 600 positions 13.3 us whole,
+// 12.3 cut, over 300 11.1 and 11.8; 16 trees of 7 nodes over 500 12.5 and 16.4).
 constexpr int kFewRows = 8;
-constexpr int kMinShare[2] = {4, 2}, kSplitTiles[2] = {6, 4};  // [few rows]
+constexpr int kMinShare[2] = {4, 2};    // [narrow join]
+constexpr int kSplitTiles[2] = {6, 4};  // [few rows]
 // An item's start and output, in key tiles (0: 64-node trees over 4096 positions 35.2 us, 1: 33.5,
 // 2: 31.5).
 constexpr int kItemCost = 2;
@@ -431,9 +432,8 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   else if (items * ((p.rows + kNarrowRows - 1) / kNarrowRows) <= 4 * p.grid) a.joins = std::max((int)items, 1);
   // a short cache is not split: the merge would take longer than the tiles it spares
   const int64_t most = ((int64_t)pg.max_pages * pg.page_size + kKeys - 1) / kKeys + (t.n_max + kKeys - 1) / kKeys;
-  const bool few = p.rows <= kFewRows;
-  a.min_share = kMinShare[few];
-  if (ws != nullptr && ws_bytes >= p.bytes && most > kSplitTiles[few]) {
+  a.min_share = kMinShare[a.joins > 0];
+  if (ws != nullptr && ws_bytes >= p.bytes && most > kSplitTiles[p.rows <= kFewRows]) {
     a.desc = static_cast<int4*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.ml_off);
