@@ -137,6 +137,10 @@ struct PagedWork {
     while (x < x1) {
       for (;;) {
         if (x >= before + total) {
+          if (chunk + 32 >= a.B) {  // (lengths that shrank since the sum was taken)
+            x = x1;
+            break;
+          }
           before += total;
           load(chunk + 32);
           continue;
