@@ -46,3 +46,7 @@ def race(before, after, rounds=80):
 
 def test_lengths_that_shrink_under_way():
     race(1, 0)
+
+
+def test_lengths_that_grow_under_way():
+    race(0, 1)

@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   const int r0 = blockIdx.x * kGroup, R = min(kGroup, a.part_rows - r0);
   if ((r0 / kRows) * a.tpt + d0.w >= d0.z) return;  // no row of this row tile exists
   // part i lies in CTA c + i's first slot, the first part in the slot its CTA named
-  const int parts = min(d1.y - c + 1, kMaxParts);
+  // (no CTA after the last has any: lengths that grow under way could name one)
+  const int parts = min(min(d1.y, a.runs - 1) - c + 1, kMaxParts);
   auto slot = [&](int i) -> int64_t { return 2 * (c + i) + (i == 0 ? d1.z : 0); };
   int rp = 1;  // threads side by side over rows: the power of two from R up
   while (rp < R) rp *= 2;
