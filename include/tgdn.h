@@ -539,7 +539,12 @@ size_t tgdn_paged_tree_attention_workspace_bytes(const tgdn_tree* tree, int32_t 
  * withhold_item % H_v), so that the consumer's wait for it expires: the CTA that owns
  * that item stops,
  * reports every item it owns as TGDN_SEQ_TIMEOUT, waits for its own copies and
- * products to finish and returns; other CTAs are unaffected.  Process-wide, not
+ * products to finish and returns; other CTAs are unaffected.  In
+ * tgdn_prompt_attention and tgdn_paged_tree_attention wait_limit_ns holds for the copies'
+ * waits for room (others keep the default), and with withhold_item >= 0 the queries of
+ * sequence withhold_item / H_kv, key/value head withhold_item % H_kv are never fetched: the
+ * CTAs that hold them stop and report the sequences of all items that they took on and had
+ * not put out.  Process-wide, not
  * thread-safe with concurrent launches; tgdn_debug_set_wait_hooks(0, -1) restores
  * the defaults.  Returns TGDN_OK, or TGDN_EINVAL for wait_limit_ns above 2 s or
  * withhold_item < -1. */

@@ -46,7 +46,9 @@
 // tiles land on barriers of the fix warps' own: a warp that only sees some of the tiles
 // could not tell a ring slot's phase from the one after next.
 //
-// Every wait is bounded; on expiry the sequence is marked TGDN_SEQ_TIMEOUT.
+// Every wait is bounded.  On expiry the CTA stops and marks the sequences of all its items from
+// the first one that its softmax warps have not all put out, those known ahead and those still
+// to come among them, TGDN_SEQ_TIMEOUT.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -129,7 +131,20 @@ struct Args {
   int part_rows;                   // rows per partial slot
   int min_share;                   // least key tiles per CTA
   int runs, joins;                 // CTAs of the attention kernel; of a narrow join per row group
+  int hold_b, hold_h;              // sequence and head whose queries never come (test hook), or -1
+  uint64_t wait_ns;                // limit of the copy warp's waits
 };
+// (hold_* and wait_ns of Args; a limit for every wait, read from memory, took registers from all
+// the roles: 16 uneven prompts 152 -> 161 us, mixed trees 222 -> 236)
+static void set_hooks(Args& a) {
+  const WaitHooks h = wait_hooks();
+  a.hold_b = h.hold_item < 0 ? -1 : h.hold_item / a.H_kv;
+  a.hold_h = h.hold_item < 0 ? -1 : h.hold_item % a.H_kv;
+  a.wait_ns = h.wait_ns ? h.wait_ns : kWaitLimitNs;
+}
+__device__ __forceinline__ void timed_out(const Args& a, int b) {
+  atomicCAS(&a.status[b], TGDN_SEQ_OK, TGDN_SEQ_TIMEOUT);
+}
 
 // (o_wide of Args)
 static int wide_rows(const void* o, int64_t stride, int d) {
@@ -197,6 +212,16 @@ static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, vo
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return mbar_try(bar, parity) || wait_slow(bar, parity, abort);
+}
+
+// The copy warp's, whose limit a test can shorten.
+static __device__ __noinline__ bool wait_copies_slow(uint64_t* bar, uint32_t parity,
+                                                     volatile int* abort, uint64_t limit_ns) {
+  return mbar_wait_suspend(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool wait_copies(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            uint64_t limit_ns) {
+  return mbar_try(bar, parity) || wait_copies_slow(bar, parity, abort, limit_ns);
 }
 
 // The product warp's waits and arrivals take shared-memory addresses (its own instructions
@@ -350,7 +375,7 @@ struct alignas(16) Bars {
   int dirty[kRing], bad[kRing];
   uint32_t tmem;
   int abort;
-  int where;  // the sequence in work when a wait expired
+  int taken, put_out[8];  // at the end: items taken on; items each softmax warp is done with
 };
 
 // Paged: ancestor-or-self sets of an item's nodes (node-index space), two items' worth, and a
@@ -455,7 +480,6 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     }
     fence_mbar_init();
     br->abort = 0;
-    br->where = -1;
   }
   if (warp == kMmaWarp) tmem_alloc(&br->tmem, kTmemCols);
   if (tid >= L::kCopyWarp * 32 && tid < L::kCopyWarp * 32 + (PAGED ? 5 : 3)) {
@@ -476,13 +500,13 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     uint32_t cnt = 0, fix = 0;  // key and value tiles requested; values to be made safe
     int n_q = 0;       // items whose queries were requested
     auto slot_free = [&](uint32_t c) -> bool {
-      return c < NS || wait_bar(&br->kvempty[c % NS], ((c / NS) - 1) & 1, abort);
+      return c < NS || wait_copies(&br->kvempty[c % NS], ((c / NS) - 1) & 1, abort, a.wait_ns);
     };
     int n = 0;
     Seg s;
     for (; ok; ++n) {
       const int r = n % kRing;
-      if (n >= kRing) ok = wait_bar(&br->segempty[r], ((n / kRing) - 1) & 1, abort);
+      if (n >= kRing) ok = wait_copies(&br->segempty[r], ((n / kRing) - 1) & 1, abort, a.wait_ns);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const bool more = work.next(s);
       if (!more) s.b = -1;
@@ -571,10 +595,11 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           load(u, false, page);
         }
         if (u == s.u0) {  // the queries, once the previous item's score products are done
-          if (n > 0) ok = wait_bar(&br->qempty, (n - 1) & 1, abort);
+          if (n > 0) ok = wait_copies(&br->qempty, (n - 1) & 1, abort, a.wait_ns);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          ++n_q;
-          if (lane == 0) {
+          const bool come = s.b != a.hold_b || s.hk != a.hold_h;
+          n_q += come;
+          if (come && lane == 0) {
             const int tiles = s.e1 > s.u0 ? 2 : 1;
             mbar_arrive_expect_tx(&br->qfull, tiles * a.gbox * L::kHalves);
             for (int t = 0; t < tiles; ++t)
@@ -597,10 +622,10 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         page = next_page;
       }
     }
-    if (!ok && lane == 0) br->where = s.b;
-    while (work.finish(s))  // work that was taken over and will not be done
-      if (lane == 0) atomicCAS(&a.status[s.b], TGDN_SEQ_OK, TGDN_SEQ_TIMEOUT);
-    if (!ok) {  // let the copies in flight land before the shared memory goes (bounded)
+    if (lane == 0) br->taken = n;
+    if (!ok) {
+      work.drop();
+      // let the copies in flight land before the shared memory goes (bounded)
       for (uint32_t c = cnt > NS ? cnt - NS : 0; c < cnt; ++c)
         (void)mbar_wait(&br->kvfull[c % NS], (c / NS) & 1);
       for (uint32_t c = fix > kFixRing ? fix - kFixRing : 0; c < fix; ++c)
@@ -734,10 +759,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         kp = vp = c;
         vp.step();
         ok = __all_sync(0xffffffffu, ok) != 0;
-        if (!ok) {
-          if (lane == 0) br->where = s.b;
-          break;
-        }
+        if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&br->segempty[r]);
         continue;
@@ -776,10 +798,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         vp.step(), vp.step();
       }
       ok = __all_sync(0xffffffffu, ok) != 0;
-      if (!ok) {
-        if (lane == 0) br->where = s.b;
-        break;
-      }
+      if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&br->segempty[r]);
     }
@@ -886,7 +905,8 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
     uint32_t done = 0;
     int built = 0, alts = 0;  // items with masks; items with alternating pipelines
     bool read_by_other = false;
-    for (int n = 0; ok; ++n) {
+    int n = 0;
+    for (; ok; ++n) {
       const int r = n % kRing;
       ok = wait_bar(&br->segfull[r], (n / kRing) & 1, abort);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -1009,7 +1029,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
         // the item's last product on O_t
         if (ok) ok = wait_bar(&br->pvdone[t], (done - 1) & 1, abort);
         if (!(ok = __all_sync(0xffffffffu, ok))) {
-          if (lane == 0) br->where = s.b;
+          if (lane == 0) timed_out(a, s.b);  // (with the rest of the items at the teardown)
           break;
         }
         tc_fence_after_sync();
@@ -1123,12 +1143,16 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
       __syncwarp();
       if (lane == 0) mbar_arrive(&br->segempty[r]);
     }
+    if (lane == 0) br->put_out[warp] = n;
   }
   // ---------------- teardown
   tc_fence_before_sync();
   const bool all_ok = __syncthreads_and(ok) != 0;
-  if (!all_ok && tid == 0 && br->where >= 0)
-    atomicCAS(&a.status[br->where], TGDN_SEQ_OK, TGDN_SEQ_TIMEOUT);
+  if (!all_ok && tid == 0) {  // the items taken on and not put out (the ring still has them all)
+    int n = br->taken;
+    for (int w = 0; w < 8; ++w) n = min(n, br->put_out[w]);
+    for (; n < br->taken; ++n) timed_out(a, br->seg[n % kRing].b);
+  }
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);

@@ -132,7 +132,18 @@ struct PagedWork {
     }
   }
 
-  __device__ bool finish(Seg&) { return false; }
+  // After an early end: the sequences with work in the rest of the run, and that of the cut item,
+  // which is not named to the join.
+  __device__ void drop() {
+    if (d0.x >= 0 && lane == 0) timed_out(a, d0.x);
+    while (x < x1) {
+      const int64_t begin = before + upto - tiles;
+      if (tiles > 0 && begin < x1 && begin + tiles > x) timed_out(a, chunk + lane);
+      before += total;
+      if (before >= x1 || chunk + 32 >= a.B) return;
+      load(chunk + 32);
+    }
+  }
   __device__ bool next(Seg& s) {
     while (x < x1) {
       for (;;) {
@@ -420,6 +431,7 @@ cudaError_t launch_paged_attn(const tgdn_tree& t, const tgdn_pages& pg, int H_q,
   a.o_wide = wide_rows(o, o_stride, d);
   a.v = v_rows;
   a.v_stride = v_stride;
+  set_hooks(a);
   a.n_max = t.n_max;
   a.ps = pg.page_size;
   a.n_pages = pg.n_pages;

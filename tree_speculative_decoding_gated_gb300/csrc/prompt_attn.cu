@@ -93,7 +93,10 @@ struct PromptWork {
   __device__ int64_t answered() {
     const bool came = __all_sync(0xffffffffu, mbar_wait(bar, (asked - 1) & 1)) != 0;
     open = false;
-    if (!came) return -1;
+    if (!came) {  // (whatever was taken over is lost)
+      for (int b = lane; b < a.B; b += 32) timed_out(a, b);
+      return -1;
+    }
     uint32_t got, cta;
     asm volatile(
         "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
@@ -158,16 +161,15 @@ struct PromptWork {
     }
     return false;
   }
-  // After an early end: the items taken over and not done, one at a time.  No request stays
-  // open when the shared memory goes.
-  __device__ bool finish(Seg& s) {
+  // After an early end: the items taken over and not done.  No request stays open when the
+  // shared memory goes.
+  __device__ void drop() {
     while (x >= 0 || open) {
       if (x < 0) x = answered();
-      const bool found = x >= 0 && find(s);
+      Seg s;
+      if (x >= 0 && find(s) && lane == 0) timed_out(a, s.b);
       x = -1;
-      if (found) return true;
     }
-    return false;
   }
 };
 
@@ -222,6 +224,7 @@ cudaError_t launch_prompt_attn(int B, int T, int H_q, int H_kv, int d, int io, f
   a.o_wide = wide_rows(o, o_stride, d);
   a.v = v_rows;
   a.v_stride = v_stride;
+  set_hooks(a);
   // At most T / blk + B blocks per head.  One row tile per item when two would leave SMs idle,
   // and with small heads, whose alternating pipelines lose least, while items are few: 5000
   // tokens, 16 heads of 64 elements 67 us after 76, 16000 tokens, 4 heads 148 after 186; at

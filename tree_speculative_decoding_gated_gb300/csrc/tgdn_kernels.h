@@ -78,7 +78,7 @@ struct OutMaps {
 bool encode_out_maps(OutMaps* m, float* U, void* o, int T, int H_v);
 // Test hooks of the bounded device waits (tgdn_debug_set_wait_hooks): a shorter wait
 // limit (0: the default) and a work item whose hand-over the 64-node kernel's producer
-// withholds (-1: none).
+// (the attention kernels' copy warp, whose waits have the limit) withholds (-1: none).
 struct WaitHooks {
   uint64_t wait_ns;
   int hold_item;

@@ -582,7 +582,8 @@ def paged_tree_attention(tree: Tree, pages: Pages, q, k_tree, v_tree, k_pages, v
 def debug_set_wait_hooks(wait_limit_ns: int = 0, withhold_item: int = -1) -> None:
     """tgdn_debug_set_wait_hooks: a test hook that shortens the bounded device waits of the
     64-node verification kernel and makes its producer withhold one work item's first
-    product, so that the consumer's wait expires (TGDN_SEQ_TIMEOUT, no fault or hang).
-    debug_set_wait_hooks() restores the defaults."""
+    product, so that the consumer's wait expires (TGDN_SEQ_TIMEOUT, no fault or hang).  In
+    prompt and paged attention the queries of sequence withhold_item // H_kv, key/value head
+    withhold_item % H_kv never come.  debug_set_wait_hooks() restores the defaults."""
     _check(lib().tgdn_debug_set_wait_hooks(int(wait_limit_ns), int(withhold_item)),
            "tgdn_debug_set_wait_hooks")
