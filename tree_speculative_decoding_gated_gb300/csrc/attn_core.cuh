@@ -940,6 +940,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&br->sread[t]);
+            __syncwarp();  // (tensor-memory accesses take the whole warp together)
           }
           // masks; the maxima again where they apply
           bool masked = false;
@@ -990,6 +991,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
             if (need) m = mx[0];
             la.x *= alpha, la.y *= alpha, lb.x *= alpha, lb.y *= alpha;
             if (u > first) {  // (the last product on O_t is done)
+              __syncwarp();
 #pragma unroll 1
               for (int q = 0; q < DP / 16; ++q) {
                 float o[16];
@@ -1022,6 +1024,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
               tc_fence_before_sync();
               __syncwarp();
               if (lane == 0) mbar_arrive(&br->pready[t][q >> 1]);
+              __syncwarp();
             }
           }
           ++done;
@@ -1122,7 +1125,7 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
           for (int q = 0; q < DP / 32; ++q) {
-            if (DP == 64) __syncwarp();  // (6 prompts of up to 2500 tokens: 44.0 -> 41.8 us)
+            __syncwarp();  // (`put` parts the warp, and the load takes all of it together)
             float o[32];
             tmem_ld32(tO + q * 32, o);
             ld_wait32(o);
