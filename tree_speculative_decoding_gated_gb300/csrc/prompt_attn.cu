@@ -62,14 +62,18 @@ struct PromptWork {
     N = good ? hi - lo : 0;
     return good;
   }
-  static __device__ void first(const Args& a, int ft, int) {
-    if (blockIdx.x != 0 || ft >= 32) return;
+  // The status words (whole warp), once per launch: by CTA 0 or, should that be taken over before
+  // it starts (nothing promises that it starts first), by the CTA that takes it over.
+  static __device__ __noinline__ void write_status(const Args& a, int lane) {
     int high = 0;
     for (int c = 0; c < a.B; c += 32) {
       int lo, N;
-      const bool good = range_of(a, c, high, ft, lo, N, high);
-      if (c + ft < a.B) a.status[c + ft] = good ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
+      const bool good = range_of(a, c, high, lane, lo, N, high);
+      if (c + lane < a.B) a.status[c + lane] = good ? TGDN_SEQ_OK : TGDN_SEQ_BAD_RANGE;
     }
+  }
+  static __device__ void first(const Args& a, int ft, int) {
+    if (blockIdx.x == 0 && ft < 32) write_status(a, ft);
   }
   static __device__ void last(const Args&, int, int) {}
 
@@ -108,6 +112,7 @@ struct PromptWork {
         : "r"(smem_addr(answer))
         : "memory");
     __syncwarp();
+    if (got && cta == 0) write_status(a, lane);
     return got ? (int64_t)cta : -1;
   }
   // Item x, if there is one (numbers mostly ascend: the search goes on where the last ended).
