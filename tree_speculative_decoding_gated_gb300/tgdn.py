@@ -216,7 +216,8 @@ class Dims:
 
 class _Handle:
     """Device tensors behind a C struct.  The struct is made (and every tensor checked) again
-    whenever an attribute is set or a tensor's storage has moved."""
+    whenever an attribute is set or anything that the checks look at has changed: a tensor's
+    address, place, type, size or contiguity."""
 
     _tensors: tuple = ()
 
@@ -226,10 +227,13 @@ class _Handle:
 
     def c(self):
         d = self.__dict__
-        at = [d[n].data_ptr() for n in self._tensors]
-        if d["_struct"] is None or d["_at"] != at:
+        seen = []
+        for n in self._tensors:
+            t = d[n]
+            seen += t.data_ptr(), t.is_cuda, t.dtype, t.numel(), t.is_contiguous()
+        if d["_struct"] is None or d["_seen"] != seen:
             d["_struct"] = self._make()
-            d["_at"] = at
+            d["_seen"] = seen
         return d["_struct"]
 
 
