@@ -3,11 +3,12 @@
 // A decode step makes several of these calls per layer, and a call's kernels take 3-15 us;
 // reading the tensors' types, shapes and addresses here instead of in Python takes ~0.5 us of
 // host time per call instead of ~6 (rotation of 33 rows: 2.8 us a call after 9.6).  Every
-// tensor is checked, so that no host pointer and no wrong layout reaches a kernel; what is wrong
-// is raised as TypeError or ValueError with the argument's name.  Each function returns the
-// call's tgdn_status.
+// tensor is checked, so that no host pointer, no other device's and no wrong layout reaches a
+// kernel; what is wrong is raised as TypeError or ValueError with the argument's name.  Each
+// function returns the call's tgdn_status.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -45,10 +46,23 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// The current device, looked up once per call (under the interpreter's lock); 0 without any.
+int g_device = -1;
+int current_device() {
+  if (g_device < 0) {
+    c10::DeviceIndex d = 0;
+    g_device = c10::cuda::GetDevice(&d) == cudaSuccess ? d : 0;
+  }
+  return g_device;
+}
+
 const at::Tensor& on_device(PyObject* o, at::ScalarType type, const char* name) {
   const at::Tensor& t = tensor(o, name);
   if (!t.is_cuda())
     raise(PyExc_ValueError, "%s: must be a CUDA tensor (the library takes device pointers)", name);
+  if (t.get_device() != current_device())
+    raise(PyExc_ValueError, "%s: on cuda:%d, the current device is cuda:%d (where the call runs)", name,
+          (int)t.get_device(), current_device());
   if (t.scalar_type() != type)
     raise(PyExc_TypeError, "%s: dtype %s, expected %s", name, name_of(t.scalar_type()), name_of(type));
   return t;
@@ -394,6 +408,7 @@ int paged_tree_attention(PyObject* const* a) {
 // Python's entry: the arguments counted, C++ exceptions turned into Python's.
 template <int (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  g_device = -1;
   try {
     if (n != N) raise(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
     return PyLong_FromLong(F(args));
