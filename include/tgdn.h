@@ -501,6 +501,9 @@ int tgdn_pages_free(const tgdn_pages* pages, int32_t n, const int32_t* seq,
 /* Moves the live pages together: with n_live pages in use, the i-th page in use from
  * n_live on moves to the i-th free page below it, in every layer, and the tables follow.
  * Afterwards pages n_live .. n_pages - 1 are free.  *n_live (device int32) is written.
+ * Inconsistent len / held, an entry outside the pool, or one that names a free page past
+ * n_live: TGDN_SEQ_BAD_PAGE; the sequence's other entries follow all the same, so that it
+ * reads what it read before.
  * Returns TGDN_OK, TGDN_EINVAL, TGDN_ETOOBIG or TGDN_ECUDA. */
 int tgdn_pages_compact(const tgdn_pages* pages, const tgdn_pool* pool, int32_t* n_live,
                        void* ws, tgdn_stream_t stream);

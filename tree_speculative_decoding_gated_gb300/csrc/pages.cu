@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(256) pages_compact_kernel(tgdn_pages p, tgdn_p
   for (int b = blockIdx.x * 8 + (tid >> 5); b < p.B; b += gridDim.x * 8) {
     const int held = p.held[b];
     bool good = sound(p, p.len[b], held);
-    for (int j = tid & 31; good && j < held; j += 32) {
+    // (every entry that names a moved page follows it, whatever else is wrong with the sequence)
+    for (int j = tid & 31; j < min(held, p.max_pages); j += 32) {
       int32_t* e = p.table + (int64_t)b * p.max_pages + j;
       const int page = *e;
       if (page < 0 || page >= p.n_pages || (page >= live && w.c[page] < 0)) good = false;
