@@ -494,7 +494,8 @@ int tgdn_pages_fork(const tgdn_pages* pages, const tgdn_pool* pool, int32_t n,
 
 /* Releases every page of sequences seq[0 .. n-1] (len = held = 0); a page that no other
  * sequence names becomes free.  Indices outside [0, B) are passed over, repeated ones
- * release once.  Returns TGDN_OK, TGDN_EINVAL or TGDN_ECUDA. */
+ * release once.  A held outside 0 .. max_pages: TGDN_SEQ_BAD_PAGE, nothing is released; an
+ * entry that names no page in use: TGDN_SEQ_BAD_PAGE, the others are released.  Returns TGDN_OK, TGDN_EINVAL or TGDN_ECUDA. */
 int tgdn_pages_free(const tgdn_pages* pages, int32_t n, const int32_t* seq,
                     tgdn_stream_t stream);
 

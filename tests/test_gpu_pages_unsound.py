@@ -55,3 +55,19 @@ def test_compaction_follows_every_entry_of_an_unsound_sequence():
         assert torch.equal(contents(p, pool, b, c), before[b]), b
     assert p.table[1, [2, 33]].tolist() == [p.n_pages, -5]
     assert p.len[0] == 641 and p.held[3] == p.max_pages + 4
+
+
+@pytest.mark.parametrize("held", [-3, 7, 1000])
+def test_free_refuses_a_count_outside_the_table(held):
+    """Columns past the sequence's own pages keep old numbers, which other sequences hold now."""
+    p, pool, rows = cache([2, 6, 4], cols=6)
+    p.table[0, 2:] = p.table[1, :4]   # old numbers
+    p.held[0] = held
+    before = [x.clone() for x in (p.table, p.len, p.held, p.refs)]
+    tgdn.pages_free(p, ints([0]))
+    assert p.status.tolist() == [BAD_PAGE, OK, OK]
+    assert all(torch.equal(a, b) for a, b in zip(before, (p.table, p.len, p.held, p.refs)))
+    p.held[0] = 2
+    tgdn.pages_free(p, ints([0, 2]))
+    assert p.status.tolist() == [OK] * 3 and p.held.tolist() == [0, 6, 0]
+    assert int(p.refs.sum()) == 6 and bool((p.refs[rows[1]] == 1).all())

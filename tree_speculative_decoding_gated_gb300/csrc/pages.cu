@@ -429,12 +429,19 @@ __global__ void __launch_bounds__(128) pages_free_kernel(tgdn_pages p, const int
   const int b = seq[blockIdx.x], tid = threadIdx.x;
   if (b < 0 || b >= p.B) return;
   if (tid == 0) {
-    s_held = atomicExch(&p.held[b], 0);  // whoever takes the count releases the pages
-    p.len[b] = 0;
-    p.status[b] = TGDN_SEQ_OK;
+    const int held = p.held[b];
+    if (held < 0 || held > p.max_pages) {
+      // left as it is: past its own pages a row keeps old numbers, which others may hold now
+      s_held = 0;
+      p.status[b] = TGDN_SEQ_BAD_PAGE;
+    } else {
+      s_held = atomicExch(&p.held[b], 0);  // whoever takes the count releases the pages
+      p.len[b] = 0;
+      p.status[b] = TGDN_SEQ_OK;
+    }
   }
   __syncthreads();
-  const int held = min(s_held, p.max_pages);
+  const int held = s_held;
   for (int j = tid; j < held; j += 128) {
     const int page = p.table[(int64_t)b * p.max_pages + j];
     if (page < 0 || page >= p.n_pages || atomicSub(&p.refs[page], 1) <= 0) {
