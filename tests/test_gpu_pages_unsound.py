@@ -71,3 +71,13 @@ def test_free_refuses_a_count_outside_the_table(held):
     tgdn.pages_free(p, ints([0, 2]))
     assert p.status.tolist() == [OK] * 3 and p.held.tolist() == [0, 6, 0]
     assert int(p.refs.sum()) == 6 and bool((p.refs[rows[1]] == 1).all())
+
+
+def test_a_sequence_listed_again_keeps_its_status():
+    p, pool, rows = cache([3, 4])
+    p.table[0, 1] = p.n_pages
+    tgdn.pages_free(p, ints([0] * 20000 + [1, -1, 2]))
+    assert p.status.tolist() == [BAD_PAGE, OK] and p.held.tolist() == [0, 0]
+    assert int(p.refs.sum()) == 1 and p.refs[rows[0][1]] == 1
+    tgdn.pages_free(p, ints([0, 0]))
+    assert p.status.tolist() == [OK, OK]

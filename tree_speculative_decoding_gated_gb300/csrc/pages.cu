@@ -425,29 +425,33 @@ cudaError_t launch_pages_fork(const tgdn_pages& p, const tgdn_pool& pool, int n,
 __global__ void __launch_bounds__(128) pages_free_kernel(tgdn_pages p, const int32_t* seq) {
   grid_launch_dependents();
   grid_dependency_wait();
-  __shared__ int s_held;
   const int b = seq[blockIdx.x], tid = threadIdx.x;
   if (b < 0 || b >= p.B) return;
-  if (tid == 0) {
-    const int held = p.held[b];
-    if (held < 0 || held > p.max_pages) {
-      // left as it is: past its own pages a row keeps old numbers, which others may hold now
-      s_held = 0;
-      p.status[b] = TGDN_SEQ_BAD_PAGE;
-    } else {
-      s_held = atomicExch(&p.held[b], 0);  // whoever takes the count releases the pages
-      p.len[b] = 0;
-      p.status[b] = TGDN_SEQ_OK;
-    }
+  // a sequence listed again is released by its first place in the list
+  bool again = false;
+  for (int j = tid; j < (int)blockIdx.x; j += 128) again |= seq[j] == b;
+  const int held = p.held[b];
+  if (__syncthreads_or(again)) return;
+  if (held < 0 || held > p.max_pages) {
+    // left as it is: past its own pages a row keeps old numbers, which others may hold now
+    if (tid == 0) p.status[b] = TGDN_SEQ_BAD_PAGE;
+    return;
   }
-  __syncthreads();
-  const int held = s_held;
+  bool bad = false;
   for (int j = tid; j < held; j += 128) {
     const int page = p.table[(int64_t)b * p.max_pages + j];
-    if (page < 0 || page >= p.n_pages || atomicSub(&p.refs[page], 1) <= 0) {
-      if (page >= 0 && page < p.n_pages) atomicAdd(&p.refs[page], 1);
-      p.status[b] = TGDN_SEQ_BAD_PAGE;
+    if (page < 0 || page >= p.n_pages) {
+      bad = true;
+    } else if (atomicSub(&p.refs[page], 1) <= 0) {
+      atomicAdd(&p.refs[page], 1);
+      bad = true;
     }
+  }
+  bad = __syncthreads_or(bad) != 0;
+  if (tid == 0) {
+    p.held[b] = 0;
+    p.len[b] = 0;
+    p.status[b] = bad ? TGDN_SEQ_BAD_PAGE : TGDN_SEQ_OK;
   }
 }
 
