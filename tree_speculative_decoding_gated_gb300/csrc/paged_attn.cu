@@ -49,7 +49,7 @@ __device__ __forceinline__ Plan plan_of(const Args& a, int b) {
   p.st = a.status[b];
   p.P = a.len[b];
   const int held = a.held[b];
-  p.N = hi - p.lo;
+  p.N = hi > p.lo ? hi - p.lo : 0;  // (far apart the wrong way round the difference would wrap)
   // (words this kernel itself may write count as planned: every CTA plans the same work)
   const bool run = p.st == TGDN_SEQ_OK || p.st == TGDN_SEQ_TIMEOUT || p.st == TGDN_SEQ_BAD_PAGE;
   if (!run || p.lo < 0 || p.N <= 0 || hi > a.T || p.N > a.n_max || p.P < 0 || held < 0 ||
