@@ -426,7 +426,8 @@ size_t tgdn_prompt_attention_workspace_bytes(int32_t B, int32_t T, int32_t H_q, 
  * all attention layers.  Position p of sequence b lies in page table[b][p / page_size].
  *   B          rows of the table (sequences)
  *   n_pages    pages of the pool; page_size positions per page: 16, 32, 64, 128 or 256
- *   max_pages  columns of the table
+ *   max_pages  columns of the table: at most 2^24, and max_pages * page_size at most
+ *              2^31 - 128 (positions are int32)
  *   table  [B][max_pages] int32;  columns past held[b] keep what they had
  *   len    [B] cached positions, 0 .. held * page_size
  *   held   [B] pages in the table row, 0 .. max_pages

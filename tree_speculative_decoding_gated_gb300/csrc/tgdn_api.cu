@@ -440,6 +440,8 @@ int check_pages(const tgdn_pages* p) {
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) != 0)
     return TGDN_EINVAL;
   if (p->n_pages > (1 << 28) || p->max_pages > (1 << 24) || p->B > (1 << 24)) return TGDN_ETOOBIG;
+  // (positions, rounded up to a key tile of 128, are int32)
+  if ((int64_t)p->max_pages * p->page_size > 0x7fffffff - 127) return TGDN_ETOOBIG;
   if (p->B > 0 && (!p->len || !p->held || !p->status || (p->max_pages > 0 && !p->table)))
     return TGDN_EINVAL;
   if (p->n_pages > 0 && !p->refs) return TGDN_EINVAL;
