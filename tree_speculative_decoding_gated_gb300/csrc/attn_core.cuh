@@ -1097,7 +1097,6 @@ __device__ __forceinline__ void pipeline(uint8_t* smem, const Args& a, const CUt
           tc_fence_after_sync();
           const float2 w = br->alt_ml[row];
           const bool dirty = *reinterpret_cast<volatile int*>(&br->dirty[r]) != 0;
-          const uint32_t tO0 = tmem + L::kColO + lanes;
           constexpr int kFirst = (DP / 32 + 1) / 2;  // pipeline 0's share, 32 columns apiece
 #pragma unroll 1
           for (int q = t == 0 ? 0 : kFirst; q < (t == 0 ? kFirst : DP / 32); ++q) {
