@@ -26,8 +26,9 @@
 // What bounds it.  d = 128: the tensor core.  A 128-key step of both pipelines is 32
 // instructions of 64 cycles (2048) and measures 2724: P lies over S, so S_t waits until
 // P_t V is done, twice a step, and the product warp's own instructions fill the rest (a
-// 32768-token prompt, 16 heads over 4: 2.44 ms, 1801 TFLOP/s, 92% of the measured library
-// rate).  Heads up to 64: the softmax; 32,768 exponentials are 1024 cycles a step and the
+// 32768-token prompt, 16 heads over 4: 2.6-2.8 ms call after call, where the power cap sets the
+// clock, 1570-1690 TFLOP/s, 80-86% of the measured library burst and 90-97% of its sustained
+// rate; 2.40 ms for the first few calls at full clock).  Heads up to 64: the softmax; 32,768 exponentials are 1024 cycles a step and the
 // whole of it ~2400, against 1280 of products.  There P has columns of its own, the next
 // S_t goes out as soon as the threads hold the last one, and two product warps keep up with
 // the shorter products (8192 tokens, 16 heads: 174 -> 147 us).  Tried and slower: two

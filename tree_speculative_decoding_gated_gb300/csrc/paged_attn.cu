@@ -15,10 +15,12 @@
 //
 // Measured: single tokens over up to 131072 positions (8 sequences, 2 heads of 128, fp16)
 // 104 us for 622 MB, 89% of the copy bandwidth.  64-node trees over up to 4096 positions
-// (16 sequences) 31 us for 65 MB: start, one cut and the join, ~12 us, weigh as much as
-// the tiles.  A batch of 17- and 129-node trees over up to 8100 positions 220 us: 129 nodes
-// of four heads are five row tiles in three blocks, whose reads of the same keys lie apart
-// in time (1057 MB for 491), and whose products take ~200 us.
+// (16 sequences) 32 us for 65 MB: a CTA has at most 7 steps of two row tiles, under 10 us;
+// the start takes ~5, and the parts of cut items (128 KB each in fp32) are 23 MB written
+// and read again by a join of ~9 us when it runs alone.  A batch of 17- and 129-node trees
+// over up to 8100 positions 222 us: 129 nodes of four heads are five row tiles in three
+// blocks, which read the same keys at times of their own (1052 MB from DRAM for 491, 27% L2
+// hits): a step takes 1.96 us where one whose keys are there takes 1.4.
 #include <algorithm>
 
 #include "attn_core.cuh"

@@ -6,8 +6,9 @@
 // writes a plan to the workspace; the kernel after it, which moves the data, spreads over
 // the device.  Copies are bound by memory: 16-byte pieces, read and written once.
 //
-// Measured: compaction of a pool of 9 layers (455 MB moved and read) 72 us of kernels, 65 of
-// them the copies at 7.0 TB/s; a branch's life (24 forks, reserve, append of paths in 9
+// Measured: compaction of a pool of 9 layers (455 MB read and written) 72 us of kernels, 65 of
+// them the copies at 7.0 TB/s (a plain copy runs at 6.7; some of what is written stays in L2);
+// a branch's life (24 forks, reserve, append of paths in 9
 // layers, free) 22 us of kernels for 35 MB: six small launches, 3-4 us each, which are
 // chained so that each is set up while the one before drains.
 #include "launch_after.cuh"

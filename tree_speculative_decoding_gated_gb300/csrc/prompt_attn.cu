@@ -11,10 +11,10 @@
 // little by the requests (6 prompts of up to 2500 tokens, d = 64: 49.5 us after 46.5).
 //
 // Bound by the tensor core (d = 128) or the softmax (d = 64), as attn_core.cuh says: a
-// 32768-token prompt 2.44 ms (1801 TFLOP/s of the visible half), 16 uneven prompts 146 us
-// (1210), where the diagonal tiles, half masked, and the items' ends take the rest; 6
-// prompts at d = 64 41 us (420).  One prompt of 97 tokens takes 6.5 us: a launch, the first
-// copies, one tile, the output.
+// 32768-token prompt 2.6-2.8 ms (1570-1690 TFLOP/s of the visible half), 16 uneven prompts
+// 151 us (1170), where the diagonal tiles, half masked, and the items' ends take the rest; 6
+// prompts at d = 64 39-40 us (430).  One prompt of 97 tokens takes 6.7 us: a launch, the
+// first copies, one tile, the output.
 #include "attn_core.cuh"
 
 namespace tgdn {

@@ -9,7 +9,7 @@
 // each thread turns 16-byte pieces (in the half layout the two pieces of its pairs).
 // Measured: 16384 rows of 20 heads of 128 (bf16, half of each head turned, 168 MB) 33 us,
 // 5.1 TB/s, 76% of the copy bandwidth (43.6 us before the loads went ahead of the angles);
-// 33 rows 3.1 us, a launch and two rounds of loads.
+// 33 rows 2.9 us, a launch and two rounds of loads.
 #include <cuda_fp16.h>
 
 #include "launch_after.cuh"
